@@ -78,6 +78,23 @@ typedef enum {
 
 enum { NVFP4_FLAG_FORCE_TWO_KERNEL = 1u }; /* skip the fused amax kernel */
 
+/* How the lines of an operand (or of the norm's output) are stored. */
+typedef enum {
+  NVFP4_FMT_NONE = 0,
+  NVFP4_FMT_E4M3 = 1, /* one E4M3 byte an element, one amax a line (or one for
+                         the tensor), no block scales: value = byte * a / 448  */
+  NVFP4_FMT_NVFP4 = 2 /* packed codes, block scales and amax, as above          */
+} nvfp4_format;
+
+/* Activation of the product's epilogue. */
+typedef enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_GELU = 1,  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))       */
+  NVFP4_ACT_SILU = 2,  /* z / (1 + e^-z)                                        */
+  NVFP4_ACT_RELU2 = 3, /* max(z, 0)^2                                           */
+  NVFP4_ACT_SWIGLU = 4 /* gated: silu(z_gate) * z_up, two lines of B an output  */
+} nvfp4_act;
+
 /* Which amax kernels nvfp4_amax_rowcol runs for these arguments.
  * Returns 1 for the fused row+column pass, 2 for the separate row / column
  * kernels, 0 when neither vector is requested. Host-only; enqueues nothing.
@@ -264,6 +281,102 @@ int nvfp4_dequantize(const uint8_t* q, const uint8_t* sc, int64_t R, int64_t C, 
 int nvfp4_quantize_dequantize(const void* x, int in_dtype, int64_t M, int64_t K, int row_mode,
                               const float* row_amax, float bound, uint8_t* q_row, uint8_t* s_row,
                               void* y, int out_dtype, const float* noop, void* stream);
+
+/* Product of two packed operands with bias, activation and residual in its
+ * epilogue (the row-scaled backward PR's general GEMM and its outer-product
+ * post-scale: out x amax_A x amax_B; the operation itself is defined here).
+ *   z_ij = (a_i f_A) (b_j f_B) sum_k u_ik v_jk + bias_j
+ *   y_ij = act(z_ij) + residual_ij
+ * u_ik is line i of A as stored: e2m1(code) * e4m3(block byte), or the E4M3
+ * value for FMT_E4M3; v_jk alike for B (always NVFP4). f = 1 / (bound * 6),
+ * or 1 / 448 for E4M3 lines. Both operands lie line by line along k, so the
+ * three products of training are all of this form:
+ *   forward          Y  = X W^T    A = rowwise X,      B = rowwise W
+ *   data gradient    dX = dY W     A = rowwise dY,     B = columnwise W
+ *   weight gradient  dW = dY^T X   A = columnwise dY,  B = columnwise X
+ * The products u v are exact, sums are FP32 in an order that depends on the
+ * sizes alone (equal calls give equal bits); the amax factors, the bias, the
+ * activation and the residual follow in FP32 and each output is rounded once.
+ *   a_fmt   NVFP4_FMT_NVFP4 or NVFP4_FMT_E4M3
+ *   a       [M][ceil(K/2)] codes, or [M][K] E4M3 bytes
+ *   a_scale [M][ceil(K/16)], NULL for E4M3
+ *   a_mode / a_amax: TENSOR ([1]) or LINE ([M]); ROWGROUP has no single factor
+ *           per line and is NVFP4_ERR_UNSUPPORTED
+ *   a_bound the bound the operand was quantized with (ignored for E4M3)
+ *   b, b_scale, b_mode, b_amax, b_bound: B's N lines (2 N for ACT_SWIGLU: N
+ *           gate lines, then the N up lines of the same outputs), NVFP4
+ *   bias    [N] ([2 N] for ACT_SWIGLU) of bias_dtype, or NULL
+ *   residual [M][N] of out_dtype, or NULL; may be y's own buffer (adding to
+ *           a main gradient in place)
+ *   z       [M][N] ([M][2 N] for ACT_SWIGLU) of out_dtype, or NULL: the value
+ *           before the activation, for nvfp4_act_backward
+ *   y       [M][N] of out_dtype (NVFP4_BF16 or NVFP4_FP32)
+ *   workspace: device memory of at least nvfp4_gemm_workspace bytes, 16-byte
+ *           aligned (NULL where that is 0); contents are scratch
+ * M, N, K >= 1, any values and any alignment of the operands. Tensors with
+ * more than 2^31 - 1 tiles of the kernel's grid are NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, const float* a_amax,
+               float a_bound, const uint8_t* b, const uint8_t* b_scale, int b_mode,
+               const float* b_amax, float b_bound, int64_t M, int64_t N, int64_t K,
+               const void* bias, int bias_dtype, int act, const void* residual, void* z, void* y,
+               int out_dtype, void* workspace, int64_t workspace_bytes, const float* noop,
+               void* stream);
+
+/* Workspace bytes nvfp4_gemm needs for these arguments (host-only; 0 for bad
+ * arguments, which nvfp4_gemm itself rejects). */
+int64_t nvfp4_gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act);
+
+/* Backward pass of nvfp4_gemm's epilogue:
+ *   dz_ij   = dy_ij act'(z_ij);  ACT_SWIGLU, z = [g | u]:
+ *             dz = [dy u silu'(g) | dy silu(g)]
+ *   dbias_j = sum_i dz_ij (of the FP32 dz, in an order that depends on the
+ *             sizes alone)
+ *   dy [M][N], z and dz [M][N] ([M][2 N] for ACT_SWIGLU), all of dtype; dz may
+ *   be z's own buffer. dbias [N] ([2 N]) float or NULL. The residual's gradient
+ *   is dy itself.
+ *   workspace: nvfp4_act_backward_workspace bytes, needed with dbias only.
+ * N above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_act_backward(const void* dy, const void* z, int dtype, int64_t M, int64_t N, int act,
+                       void* dz, float* dbias, void* workspace, int64_t workspace_bytes,
+                       const float* noop, void* stream);
+int64_t nvfp4_act_backward_workspace(int64_t M, int64_t N, int act);
+
+/* Root-mean-square norm with the residual's addition, quantized on the way
+ * out, one read of the row:
+ *   h_k = x_k + residual_k (FP32);  r = 1 / sqrt(sum_k h_k^2 / K + eps)
+ *   y_k = h_k r w_k;  row_amax = max_k |y_k|
+ *   q_fmt E4M3:  q [M][K], E4M3_RNE(min(RN(y S), 448) with the sign kept),
+ *                S = amax == 0 ? 1 : min(RN(448 / amax), FLT_MAX)
+ *   q_fmt NVFP4: q [M][ceil(K/2)], s [M][ceil(K/16)]: the rowwise copy that
+ *                nvfp4_quantize_transpose makes of the FP32 y, mode LINE
+ * Either is an A operand of nvfp4_gemm.
+ *   x, residual (or NULL) [M][K] of in_dtype; weight [K] of w_dtype; eps >= 0
+ *   h [M][K] of in_dtype or NULL: the sum, rounded (may be x or residual)
+ *   y [M][K] of y_dtype or NULL; rstd [M] float or NULL: r, for the backward
+ *   row_amax [M] float, required with q; q_fmt NONE: q and s NULL
+ *   bound: NVFP4 only (0 < bound <= 448)
+ * At least one output. sum_k h_k^2 has to stay below FLT_MAX. K above 2^27 is
+ * NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_rmsnorm(const void* x, const void* residual, int in_dtype, const void* weight,
+                  int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y, int y_dtype,
+                  float* rstd, int q_fmt, uint8_t* q, uint8_t* s, float* row_amax, float bound,
+                  const float* noop, void* stream);
+
+/* Backward pass of nvfp4_rmsnorm: with xh_k = h_k r and g_k = dy_k w_k
+ *   dx_k = r (g_k - xh_k sum_j(g_j xh_j) / K) + dres_k
+ *   dweight_k = sum over rows of dy_k xh_k (in an order that depends on the
+ *               sizes alone)
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h, dres (or NULL: the gradient that reaches h by other ways), dx
+ *   [M][K] of in_dtype, dx may be dy or dres; weight [K] of w_dtype;
+ *   rstd [M] from the forward pass; dweight [K] float or NULL
+ *   workspace: nvfp4_rmsnorm_backward_workspace bytes, needed with dweight only.
+ * K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_rmsnorm_backward(const void* dy, const void* h, int in_dtype, const void* weight,
+                           int w_dtype, const float* rstd, const void* dres, int64_t M, int64_t K,
+                           void* dx, float* dweight, void* workspace, int64_t workspace_bytes,
+                           const float* noop, void* stream);
+int64_t nvfp4_rmsnorm_backward_workspace(int64_t M, int64_t K);
 
 /* Human-readable name of a status code (static storage). */
 const char* nvfp4_status_string(int status);

@@ -37,6 +37,16 @@ NVFP4_AMAX_ROWGROUP = 2
 
 NVFP4_FLAG_FORCE_TWO_KERNEL = 1
 
+NVFP4_FMT_NONE = 0
+NVFP4_FMT_E4M3 = 1
+NVFP4_FMT_NVFP4 = 2
+
+NVFP4_ACT_NONE = 0
+NVFP4_ACT_GELU = 1
+NVFP4_ACT_SILU = 2
+NVFP4_ACT_RELU2 = 3
+NVFP4_ACT_SWIGLU = 4
+
 # Every entry point include/nvfp4.h declares.
 EXPORTED = ("nvfp4_amax_path", "nvfp4_amax_rowcol", "nvfp4_group_amax_expand",
             "nvfp4_check_group_end",
@@ -44,6 +54,9 @@ EXPORTED = ("nvfp4_amax_path", "nvfp4_amax_rowcol", "nvfp4_group_amax_expand",
             "nvfp4_quantize_2d",
             "nvfp4_quantize_grouped",
             "nvfp4_quantize_dequantize", "nvfp4_dequantize",
+            "nvfp4_gemm", "nvfp4_gemm_workspace",
+            "nvfp4_act_backward", "nvfp4_act_backward_workspace",
+            "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace",
             "nvfp4_status_string")
 
 NVFP4_GROUPS_MAX = 256
@@ -98,6 +111,23 @@ def load_library():
                                               c_int, f32p, vp]
     lib.nvfp4_dequantize.restype = c_int
     lib.nvfp4_dequantize.argtypes = [u8p, u8p, i64, i64, c_int, f32p, c_f, vp, c_int, f32p, vp]
+    lib.nvfp4_gemm.restype = c_int
+    lib.nvfp4_gemm.argtypes = [c_int, u8p, u8p, c_int, f32p, c_f, u8p, u8p, c_int, f32p, c_f,
+                               i64, i64, i64, vp, c_int, c_int, vp, vp, vp, c_int, vp, i64, f32p, vp]
+    lib.nvfp4_gemm_workspace.restype = i64
+    lib.nvfp4_gemm_workspace.argtypes = [c_int, i64, i64, i64, c_int]
+    lib.nvfp4_act_backward.restype = c_int
+    lib.nvfp4_act_backward.argtypes = [vp, vp, c_int, i64, i64, c_int, vp, f32p, vp, i64, f32p, vp]
+    lib.nvfp4_act_backward_workspace.restype = i64
+    lib.nvfp4_act_backward_workspace.argtypes = [i64, i64, c_int]
+    lib.nvfp4_rmsnorm.restype = c_int
+    lib.nvfp4_rmsnorm.argtypes = [vp, vp, c_int, vp, c_int, c_f, i64, i64, vp, vp, c_int, f32p, c_int,
+                                  u8p, u8p, f32p, c_f, f32p, vp]
+    lib.nvfp4_rmsnorm_backward.restype = c_int
+    lib.nvfp4_rmsnorm_backward.argtypes = [vp, vp, c_int, vp, c_int, f32p, vp, i64, i64, vp, f32p, vp,
+                                           i64, f32p, vp]
+    lib.nvfp4_rmsnorm_backward_workspace.restype = i64
+    lib.nvfp4_rmsnorm_backward_workspace.argtypes = [i64, i64]
     _lib = lib
     return lib
 
@@ -386,6 +416,204 @@ def nvfp4_dequantize(q: torch.Tensor, sc: torch.Tensor, R: int, C: int, amax_mod
                               ctypes.c_float(bound), _ptr(y), _dtype_code(y), _ptr(noop),
                               _stream(stream, dev))
     _check("nvfp4_dequantize", st)
+
+
+# ------------------------------------------ product, norm and their gradients
+# These run per layer and per token, so their marshalling is lean: one pass
+# over a tensor's properties, plain integers to C.
+_OUT_CODES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_FP32}
+_U8 = (torch.uint8,)
+
+
+def _arg(t, name: str, dtypes, numel: int, dev) -> Optional[int]:
+    """The device address of an optional tensor argument, checked."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in dtypes or t.numel() != numel or t.device != dev or not t.is_contiguous():
+        _dev(t, name, dtypes, numel, dev)
+    return t.data_ptr()
+
+
+def _first(t, name: str, dtypes) -> torch.device:
+    """The device of the argument that decides it for the others."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    return t.device
+
+
+def _raw_stream(stream, dev) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
+    """(tensor, address, bytes) of the workspace: the caller's (any dtype), or
+    one from torch's allocator, which orders its reuse on the stream."""
+    if need <= 0:
+        return None, None, 0
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
+    if not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    size = ws.numel() * ws.element_size()
+    if size < need:
+        raise ValueError(f"workspace must have {need} bytes, got {size}")
+    return ws, ws.data_ptr(), size
+
+
+def nvfp4_gemm_workspace(a_fmt: int, M: int, N: int, K: int, act: int = NVFP4_ACT_NONE) -> int:
+    """Workspace bytes of nvfp4_gemm."""
+    return load_library().nvfp4_gemm_workspace(a_fmt, M, N, K, act)
+
+
+def nvfp4_gemm(a: torch.Tensor, a_scale: Optional[torch.Tensor], a_mode: int, a_amax: torch.Tensor,
+               a_bound: float, b: torch.Tensor, b_scale: torch.Tensor, b_mode: int,
+               b_amax: torch.Tensor, b_bound: float, M: int, N: int, K: int, y: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, act: int = NVFP4_ACT_NONE,
+               residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, noop: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """y [M, N] = act(A B^T + bias) + residual of packed operands.
+
+    a: uint8 codes [M, ceil(K/2)] with a_scale [M, ceil(K/16)] (NVFP4), or
+    float8_e4m3fn [M, K] with a_scale None (8-bit lines). b: the N lines (2 N
+    for NVFP4_ACT_SWIGLU: gate lines, then up lines), NVFP4. y, z and residual
+    share y's dtype (bfloat16 or float32); bias is bfloat16 or float32. A
+    workspace, where the sizes need one (nvfp4_gemm_workspace), is taken from
+    torch's allocator unless given."""
+    lib = _lib or load_library()
+    dev = _first(a, "a", (torch.uint8, torch.float8_e4m3fn))
+    fmt = NVFP4_FMT_NVFP4 if a.dtype == torch.uint8 else NVFP4_FMT_E4M3
+    if fmt == NVFP4_FMT_NVFP4 and a_scale is None:
+        raise ValueError("a_scale is required for NVFP4 lines")
+    if fmt == NVFP4_FMT_E4M3 and a_scale is not None:
+        raise ValueError("a_scale must be None for E4M3 lines")
+    out = _OUT_CODES.get(getattr(y, "dtype", None))
+    if out is None:
+        raise TypeError("y must be a bfloat16 or float32 tensor")
+    NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
+    kq, ks = (K + 1) // 2, (K + 15) // 16
+    same = (y.dtype,)
+    need = lib.nvfp4_gemm_workspace(fmt, M, N, K, act)
+    ws, wp, wb = _workspace(workspace, need, dev, stream) if need > 0 else (None, None, 0)
+    st = lib.nvfp4_gemm(
+        fmt, _arg(a, "a", (a.dtype,), M * (kq if fmt == NVFP4_FMT_NVFP4 else K), dev),
+        _arg(a_scale, "a_scale", _SCALE_DTYPES, M * ks, dev), a_mode,
+        _arg(a_amax, "a_amax", _F32, M if a_mode == NVFP4_AMAX_LINE else 1, dev), a_bound,
+        _arg(b, "b", _U8, NB * kq, dev), _arg(b_scale, "b_scale", _SCALE_DTYPES, NB * ks, dev), b_mode,
+        _arg(b_amax, "b_amax", _F32, NB if b_mode == NVFP4_AMAX_LINE else 1, dev), b_bound,
+        M, N, K, _arg(bias, "bias", _OUT_CODES, NB, dev),
+        0 if bias is None else _OUT_CODES[bias.dtype], act,
+        _arg(residual, "residual", same, M * N, dev), _arg(z, "z", same, M * NB, dev),
+        _arg(y, "y", same, M * N, dev), out, wp, wb, _arg(noop, "noop", _F32, 1, dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_gemm", st)
+
+
+def nvfp4_act_backward_workspace(M: int, N: int, act: int) -> int:
+    """Workspace bytes of nvfp4_act_backward with dbias."""
+    return load_library().nvfp4_act_backward_workspace(M, N, act)
+
+
+def nvfp4_act_backward(dy: torch.Tensor, z: torch.Tensor, act: int, dz: torch.Tensor,
+                       dbias: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dz = dy * act'(z) of dy [M, N], and dbias (float32) = its sum over rows.
+    z and dz have dy's shape ([M, 2 N] for NVFP4_ACT_SWIGLU) and dtype."""
+    lib = _lib or load_library()
+    dev = _first(dy, "dy", _OUT_CODES)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D [M, N]")
+    M, N = dy.shape
+    NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
+    same = (dy.dtype,)
+    need = lib.nvfp4_act_backward_workspace(M, N, act) if dbias is not None else 0
+    ws, wp, wb = _workspace(workspace, need, dev, stream)
+    st = lib.nvfp4_act_backward(
+        _arg(dy, "dy", same, M * N, dev), _arg(z, "z", same, M * NB, dev), _OUT_CODES[dy.dtype], M, N,
+        act, _arg(dz, "dz", same, M * NB, dev), _arg(dbias, "dbias", _F32, NB, dev), wp, wb,
+        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_act_backward", st)
+
+
+def nvfp4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                  residual: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                  y: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                  q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                  row_amax: Optional[torch.Tensor] = None, bound: float = 448.0,
+                  noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h = x + residual, y = h / rms(h) * weight of x [M, K], with y's row
+    amax and codes: q float8_e4m3fn [M, K] (8-bit lines), or uint8
+    [M, ceil(K/2)] with s [M, ceil(K/16)] (NVFP4). Outputs not given are not
+    written; rstd is what nvfp4_rmsnorm_backward takes."""
+    lib = _lib or load_library()
+    dev = _first(x, "x", _OUT_CODES)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    same = (x.dtype,)
+    fmt, qn = NVFP4_FMT_NONE, 0
+    if q is not None:
+        if q.dtype == torch.float8_e4m3fn:
+            fmt, qn = NVFP4_FMT_E4M3, M * K
+        else:
+            fmt, qn = NVFP4_FMT_NVFP4, M * ((K + 1) // 2)
+    st = lib.nvfp4_rmsnorm(
+        _arg(x, "x", same, M * K, dev), _arg(residual, "residual", same, M * K, dev),
+        _OUT_CODES[x.dtype], _arg(weight, "weight", _OUT_CODES, K, dev),
+        _OUT_CODES.get(getattr(weight, "dtype", None), -1), eps, M, K, _arg(h, "h", same, M * K, dev),
+        _arg(y, "y", _OUT_CODES, M * K, dev), 0 if y is None else _OUT_CODES[y.dtype],
+        _arg(rstd, "rstd", _F32, M, dev), fmt,
+        _arg(q, "q", (torch.float8_e4m3fn, torch.uint8), qn, dev),
+        _arg(s, "s", _SCALE_DTYPES, M * ((K + 15) // 16), dev),
+        _arg(row_amax, "row_amax", _F32, M, dev), bound, _arg(noop, "noop", _F32, 1, dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_rmsnorm", st)
+
+
+def nvfp4_rmsnorm_backward_workspace(M: int, K: int) -> int:
+    """Workspace bytes of nvfp4_rmsnorm_backward with dweight."""
+    return load_library().nvfp4_rmsnorm_backward_workspace(M, K)
+
+
+def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                           rstd: torch.Tensor, dx: torch.Tensor,
+                           dweight: Optional[torch.Tensor] = None,
+                           dres: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx [M, K] and dweight [K] (float32) of nvfp4_rmsnorm from dy [M, K], the
+    saved h and rstd; dres, the gradient that reaches h by other ways, is added
+    to dx."""
+    lib = _lib or load_library()
+    dev = _first(dy, "dy", _OUT_CODES)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D [M, K]")
+    M, K = dy.shape
+    same = (dy.dtype,)
+    need = lib.nvfp4_rmsnorm_backward_workspace(M, K) if dweight is not None else 0
+    ws, wp, wb = _workspace(workspace, need, dev, stream)
+    st = lib.nvfp4_rmsnorm_backward(
+        _arg(dy, "dy", same, M * K, dev), _arg(h, "h", same, M * K, dev), _OUT_CODES[dy.dtype],
+        _arg(weight, "weight", _OUT_CODES, K, dev), _OUT_CODES.get(getattr(weight, "dtype", None), -1),
+        _arg(rstd, "rstd", _F32, M, dev), _arg(dres, "dres", same, M * K, dev), M, K,
+        _arg(dx, "dx", same, M * K, dev), _arg(dweight, "dweight", _F32, K, dev), wp, wb,
+        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_rmsnorm_backward", st)
 
 
 # --------------------------------------------------------------- conveniences

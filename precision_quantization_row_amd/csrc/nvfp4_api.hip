@@ -310,4 +310,135 @@ int nvfp4_dequantize(const uint8_t* q, const uint8_t* sc, int64_t R, int64_t C, 
   return launch_dequant(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
 }
 
+// ------------------------------------------------- product, norm, gradients
+static bool valid_dtype(int d) { return d == NVFP4_BF16 || d == NVFP4_FP32; }
+constexpr int64_t kMaxSize = (int64_t)1 << 40;   // beyond: an argument error
+constexpr int64_t kMaxCols = (int64_t)1 << 27;   // of the row-wise kernels
+
+int64_t nvfp4_gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act) {
+  if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return 0;
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return 0;
+  return gemm_workspace(a_fmt, M, N, K, act);
+}
+
+int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, const float* a_amax,
+               float a_bound, const uint8_t* b, const uint8_t* b_scale, int b_mode,
+               const float* b_amax, float b_bound, int64_t M, int64_t N, int64_t K,
+               const void* bias, int bias_dtype, int act, const void* residual, void* z, void* y,
+               int out_dtype, void* workspace, int64_t workspace_bytes, const float* noop,
+               void* stream) {
+  if (!a || !a_amax || !b || !b_scale || !b_amax || !y) return NVFP4_ERR_ARG;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
+  if (a_fmt != NVFP4_FMT_NVFP4 && a_fmt != NVFP4_FMT_E4M3) return NVFP4_ERR_ARG;
+  if ((a_fmt == NVFP4_FMT_NVFP4) != (a_scale != nullptr)) return NVFP4_ERR_ARG;
+  if (a_mode == NVFP4_AMAX_ROWGROUP || b_mode == NVFP4_AMAX_ROWGROUP) return NVFP4_ERR_UNSUPPORTED;
+  if (a_mode != NVFP4_AMAX_TENSOR && a_mode != NVFP4_AMAX_LINE) return NVFP4_ERR_ARG;
+  if (b_mode != NVFP4_AMAX_TENSOR && b_mode != NVFP4_AMAX_LINE) return NVFP4_ERR_ARG;
+  if (a_fmt == NVFP4_FMT_NVFP4 && !valid_bound(a_bound)) return NVFP4_ERR_ARG;
+  if (!valid_bound(b_bound)) return NVFP4_ERR_ARG;
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return NVFP4_ERR_ARG;
+  if (!valid_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype))) return NVFP4_ERR_ARG;
+  const int64_t need = gemm_workspace(a_fmt, M, N, K, act);
+  if (need < 0) return NVFP4_ERR_UNSUPPORTED;
+  if (need > 0 && (!workspace || workspace_bytes < need ||
+                   (reinterpret_cast<uintptr_t>(workspace) & 15) != 0))
+    return NVFP4_ERR_ARG;
+  GemmArgs g;
+  g.a = {a, a_scale, a_amax, a_mode,
+         a_fmt == NVFP4_FMT_E4M3 ? 1.0f / 448.0f : 1.0f / (a_bound * 6.0f)};
+  g.b = {b, b_scale, b_amax, b_mode, 1.0f / (b_bound * 6.0f)};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.act = act;
+  g.bias = bias;
+  g.bias_dtype = bias_dtype;
+  g.residual = residual;
+  g.z = z;
+  g.y = y;
+  g.out_dtype = out_dtype;
+  g.ws = static_cast<float*>(workspace);
+  g.noop = noop;
+  return launch_gemm(g, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int64_t nvfp4_act_backward_workspace(int64_t M, int64_t N, int act) {
+  if (M < 1 || N < 1 || M > kMaxSize || N > kMaxCols) return 0;
+  return 4 * act_bwd_parts(M, N) * (act == NVFP4_ACT_SWIGLU ? 2 * N : N);
+}
+
+int nvfp4_act_backward(const void* dy, const void* z, int dtype, int64_t M, int64_t N, int act,
+                       void* dz, float* dbias, void* workspace, int64_t workspace_bytes,
+                       const float* noop, void* stream) {
+  if (!dy || !z || !dz || M < 1 || N < 1 || M > kMaxSize || N > kMaxSize) return NVFP4_ERR_ARG;
+  if (!valid_dtype(dtype)) return NVFP4_ERR_ARG;
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return NVFP4_ERR_ARG;
+  if (N > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  if (dbias && (!workspace || workspace_bytes < nvfp4_act_backward_workspace(M, N, act) ||
+                (reinterpret_cast<uintptr_t>(workspace) & 15) != 0))
+    return NVFP4_ERR_ARG;
+  const ActBwdArgs a = {dy, z, dtype, act, M, N, dz, dbias, static_cast<float*>(workspace), noop};
+  return launch_act_bwd(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int nvfp4_rmsnorm(const void* x, const void* residual, int in_dtype, const void* weight,
+                  int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y, int y_dtype,
+                  float* rstd, int q_fmt, uint8_t* q, uint8_t* s, float* row_amax, float bound,
+                  const float* noop, void* stream) {
+  if (!x || !weight || M < 1 || K < 1 || M > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
+  if (!valid_dtype(in_dtype) || !valid_dtype(w_dtype)) return NVFP4_ERR_ARG;
+  if (!(isfinite(eps) && eps >= 0.0f)) return NVFP4_ERR_ARG;
+  if (y && !valid_dtype(y_dtype)) return NVFP4_ERR_ARG;
+  if (q_fmt != NVFP4_FMT_NONE && q_fmt != NVFP4_FMT_E4M3 && q_fmt != NVFP4_FMT_NVFP4)
+    return NVFP4_ERR_ARG;
+  if ((q_fmt != NVFP4_FMT_NONE) != (q != nullptr)) return NVFP4_ERR_ARG;
+  if ((q_fmt == NVFP4_FMT_NVFP4) != (s != nullptr)) return NVFP4_ERR_ARG;
+  if (q && !row_amax) return NVFP4_ERR_ARG;
+  if (q_fmt == NVFP4_FMT_NVFP4 && !valid_bound(bound)) return NVFP4_ERR_ARG;
+  if (!h && !y && !rstd && !row_amax) return NVFP4_ERR_ARG;
+  if (K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  NormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.in_dtype = in_dtype;
+  a.w_dtype = w_dtype;
+  a.M = M;
+  a.K = K;
+  a.eps = eps;
+  a.h = h;
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.rstd = rstd;
+  a.q_fmt = q_fmt;
+  a.q = q;
+  a.s = s;
+  a.row_amax = row_amax;
+  a.F = q_fmt == NVFP4_FMT_NVFP4 ? bound * 6.0f : 1.0f;
+  a.F_inv = 1.0f / a.F;
+  a.noop = noop;
+  return launch_norm(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int64_t nvfp4_rmsnorm_backward_workspace(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || M > kMaxSize || K > kMaxCols) return 0;
+  return 4 * norm_bwd_parts(M, K) * K;
+}
+
+int nvfp4_rmsnorm_backward(const void* dy, const void* h, int in_dtype, const void* weight,
+                           int w_dtype, const float* rstd, const void* dres, int64_t M, int64_t K,
+                           void* dx, float* dweight, void* workspace, int64_t workspace_bytes,
+                           const float* noop, void* stream) {
+  if (!dy || !h || !weight || !rstd || !dx || M < 1 || K < 1 || M > kMaxSize || K > kMaxSize)
+    return NVFP4_ERR_ARG;
+  if (!valid_dtype(in_dtype) || !valid_dtype(w_dtype)) return NVFP4_ERR_ARG;
+  if (K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  if (dweight && (!workspace || workspace_bytes < nvfp4_rmsnorm_backward_workspace(M, K) ||
+                  (reinterpret_cast<uintptr_t>(workspace) & 15) != 0))
+    return NVFP4_ERR_ARG;
+  const NormBwdArgs a = {dy,   h, weight, dres, in_dtype, w_dtype, rstd,
+                         M,    K, dx,     dweight, static_cast<float*>(workspace), noop};
+  return launch_norm_bwd(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
 }  // extern "C"

@@ -77,4 +77,78 @@ struct QdqArgs {
 };
 int launch_qdq(const QdqArgs& a, hipStream_t s);
 
+// root-mean-square norm (norm.hip)
+struct NormArgs {
+  const void *x, *residual, *w;
+  int in_dtype, w_dtype;  // 0 BF16, 1 FP32
+  int64_t M, K;
+  float eps;
+  void* h;
+  void* y;
+  int y_dtype;
+  float* rstd;
+  int q_fmt;  // 0 none, 1 E4M3, 2 NVFP4
+  uint8_t *q, *s;
+  float* row_amax;
+  float F, F_inv;
+  const float* noop;
+  int64_t row0 = 0;
+};
+int launch_norm(const NormArgs& a, hipStream_t s);
+
+struct NormBwdArgs {
+  const void *dy, *h, *w, *dres;
+  int in_dtype, w_dtype;
+  const float* rstd;
+  int64_t M, K;
+  void* dx;
+  float* dw;
+  float* part;  // [norm_bwd_parts(M, K)][K], if dw
+  const float* noop;
+};
+int64_t norm_bwd_parts(int64_t M, int64_t K);
+int launch_norm_bwd(const NormBwdArgs& a, hipStream_t s);
+
+// sums over the rows of part [P][N], in a fixed order
+int launch_colsum(const float* part, int64_t P, int64_t N, float* out, const float* noop,
+                  hipStream_t s);
+
+// backward of the product's epilogue (act.hip)
+struct ActBwdArgs {
+  const void *dy, *z;
+  int dtype;
+  int act;
+  int64_t M, N;
+  void* dz;
+  float* dbias;
+  float* part;  // [act_bwd_parts(M, N)][N or 2 N], if dbias
+  const float* noop;
+};
+int64_t act_bwd_parts(int64_t M, int64_t N);
+int launch_act_bwd(const ActBwdArgs& a, hipStream_t s);
+
+// product of packed operands (gemm.hip)
+struct GemmOperand {
+  const uint8_t* q;
+  const uint8_t* s;   // block scales, NULL for E4M3 lines
+  const float* amax;
+  int mode;           // 0 one amax, 1 one per line
+  float f_inv;        // 1 / (bound * 6), 1 / 448 for E4M3 lines
+};
+struct GemmArgs {
+  GemmOperand a, b;
+  int64_t M, N, K;
+  int act;
+  const void* bias;
+  int bias_dtype;
+  const void* residual;
+  void* z;
+  void* y;
+  int out_dtype;      // of y, z and residual
+  float* ws;
+  const float* noop;
+};
+int64_t gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act);
+int launch_gemm(const GemmArgs& a, hipStream_t s);
+
 }  // namespace nvfp4
