@@ -160,9 +160,13 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int n) {
 // last 16; both operands alike, so the sum covers every k once.
 constexpr int TM = 256, TN = 256, TK = 128;
 constexpr int TILE_BYTES = (TM + TN) * 128;  // one stage in LDS: 64 binary16 a line
-// 16-byte slot of chunk c of line r: rotated by the line so that the lanes of
-// an access, one line each, spread over the banks.
-__device__ __forceinline__ int slot(int r, int c) { return r * 128 + 16 * (c ^ (r & 7)); }
+// 16-byte slot of chunk c of line r, rotated by the line: 16 lanes that read one
+// chunk of 16 neighbouring lines touch all 64 banks once (a line is half of
+// them), and 8 lanes that write 4 chunks of 2 lines touch 8 different slots.
+// Rotated by r & 7 alone, reads took two passes (counted).
+__device__ __forceinline__ int slot(int r, int c) {
+  return r * 128 + 16 * (c ^ ((r >> 1) & 7) ^ (r & 1));
+}
 
 template <bool A8, bool GATED>
 __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int gm, int gn) {
