@@ -83,36 +83,51 @@ __device__ __forceinline__ float load_bias(const GemmArgs& p, int64_t j) {
          : p.bias_dtype == 0 ? load1(static_cast<const uint16_t*>(p.bias) + j)
                              : static_cast<const float*>(p.bias)[j];
 }
-// 8 consecutive outputs of line i from column j on, nj of them (8 or more:
-// all) in the matrix. z0: pre-activations (the gate's, if gated), z1: the up
+// 8 consecutive outputs, from column j on, of each of the lines i, i + STEP,
+// i + 2 STEP, i + 3 STEP; nj columns (8 or more: all) and the lines below M
+// are in the matrix. z0: pre-activations (the gate's, if gated), z1: the up
 // lines'; both with their bias.
-template <typename T, bool GATED>
-__device__ __forceinline__ void finish8_t(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
-                                          const float (&z0)[8], const float (&z1)[8]) {
-  if (p.z) {
-    T* z = static_cast<T*>(p.z) + i * (GATED ? 2 * p.N : p.N) + j;
-    store8(z, nj, z0);
-    if constexpr (GATED) store8(z + p.N, nj, z1);
-  }
-  float y[8];
+template <typename T, bool GATED, int STEP>
+__device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
+                                             float (&z0)[4][8], float (&z1)[GATED ? 4 : 1][8]) {
+  if (nj <= 0) return;
+  Raw8<T> res[4];
+  if (p.residual) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if constexpr (GATED) y[k] = silu_f(z0[k]) * z1[k];
-    else y[k] = act_f(p.act, z0[k]);
+    for (int v = 0; v < 4; ++v)
+      if (i + v * STEP < p.M)
+        load8_raw(static_cast<const T*>(p.residual) + (i + v * STEP) * p.N + j, nj, res[v]);
+  }
+  if (p.z) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (i + v * STEP < p.M) {
+        T* z = static_cast<T*>(p.z) + (i + v * STEP) * (GATED ? 2 * p.N : p.N) + j;
+        store8(z, nj, z0[v]);
+        if constexpr (GATED) store8(z + p.N, nj, z1[v]);
+      }
+  }
+  if constexpr (GATED) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z0[v][e] = silu_f(z0[v][e]) * z1[v][e];
+  } else if (p.act != ACT_NONE) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) act8(p.act, z0[v]);
   }
   if (p.residual) {
-    float r[8];
-    load8(static_cast<const T*>(p.residual) + i * p.N + j, nj, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] += r[k];
+    for (int v = 0; v < 4; ++v) {
+      float r[8];
+      unpack8(res[v], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z0[v][e] += r[e];
+    }
   }
-  store8(static_cast<T*>(p.y) + i * p.N + j, nj, y);
-}
-template <bool GATED>
-__device__ __forceinline__ void finish8(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
-                                        const float (&z0)[8], const float (&z1)[8]) {
-  if (p.out_dtype == 0) finish8_t<uint16_t, GATED>(p, i, j, nj, z0, z1);
-  else finish8_t<float, GATED>(p, i, j, nj, z0, z1);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (i + v * STEP < p.M) store8(static_cast<T*>(p.y) + (i + v * STEP) * p.N + j, nj, z0[v]);
 }
 
 // 16 bytes of a packed line from byte `off` on; bytes past the line's end read
@@ -305,6 +320,7 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
   };
   auto slice = [&](auto h_, auto kk_, int k, auto next_) {
     constexpr int H = decltype(h_)::value, KK = decltype(kk_)::value, NEXT = decltype(next_)::value;
+    constexpr int BAR = 4;
     constexpr int FIRST = 3 * KK, CHUNKS = KK == 2 ? 2 : KK == 3 ? 0 : 3;
     constexpr int S0 = A8 && FIRST >= 4 ? 8 : 17, S1 = A8 && FIRST + 1 >= 4 ? 8 : 17,
                   S2 = A8 && FIRST + 2 >= 4 ? 8 : 17;
@@ -317,12 +333,18 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
       constexpr int n = decltype(n_)::value, mi = n / 4, ni = n % 4;
       acc[mi][ni] =
           __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[KK & 1][ni], fa[KK & 1][mi], acc[mi][ni], 0, 0, 0);
-      if constexpr ((NEXT > 0 || KK < 3) && n < 8) {
-        constexpr int i = n >> 1;
-        if constexpr (n & 1)
+      // The reads come in the order of their use. In the last slice they follow
+      // the barrier, which stands a few matrix instructions in, when the LDS
+      // writes before it have long been done.
+      if constexpr (KK == 3 && n == BAR) __syncthreads();
+      constexpr int rd = KK == 3 ? n - BAR : n;
+      if constexpr ((NEXT > 0 || KK < 3) && rd >= 0 && rd < 8) {
+        if constexpr (rd >= 1 && rd < 5)
+          nb[rd - 1] = *reinterpret_cast<const h8*>(lf + slot(wn * 128 + (rd - 1) * 32 + l32, 2 * RK + g));
+        else {
+          constexpr int i = rd == 0 ? 0 : rd - 4;
           na[i] = *reinterpret_cast<const h8*>(lf + TN * 128 + slot(wm * 128 + i * 32 + l32, 2 * RK + g));
-        else
-          nb[i] = *reinterpret_cast<const h8*>(lf + slot(wn * 128 + i * 32 + l32, 2 * RK + g));
+        }
       }
       if constexpr (NEXT > 0 && CHUNKS > 0) {
         constexpr int Z0 = n * TOTAL / 16, Z1 = (n + 1) * TOTAL / 16;
@@ -337,7 +359,7 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
     });
   };
   auto stage = [&](auto h_, int k, auto next_) {
-    constexpr int H = decltype(h_)::value, NEXT = decltype(next_)::value;
+    constexpr int NEXT = decltype(next_)::value;
     slice(h_, std::integral_constant<int, 0>{}, k, next_);
     slice(h_, std::integral_constant<int, 1>{}, k, next_);
     slice(h_, std::integral_constant<int, 2>{}, k, next_);
@@ -345,7 +367,6 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
 #pragma unroll
       for (int i = 0; i < 8; ++i) fetch(i, k + TK, std::false_type{});
     }
-    __syncthreads();
     slice(h_, std::integral_constant<int, 3>{}, k, next_);
   };
   using C0 = std::integral_constant<int, 0>;
@@ -382,7 +403,7 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
   // 8 consecutive outputs of one line. Register r of a 32 x 32 result: line
   // l32 of A, line 8 (r / 4) + 4 g + r % 4 of B.
   float* ep = reinterpret_cast<float*>(lds) + wave * 32 * 132;
-  constexpr int LPR = GATED ? 8 : 16;  // lanes to a line
+  constexpr int LPR = GATED ? 8 : 16, RPL = 64 / LPR;  // lanes to a line, lines to a wave's access
   const int cl = 8 * (lane % LPR);
   const int64_t j = j0 + wn * (GATED ? 64 : 128) + cl, nj = p.N - j;
   LineScale w0[8], w1[8];
@@ -415,19 +436,22 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
       *reinterpret_cast<float2*>(ep + l32 * 132 + 128) = make_float2(x[mi].m, __int_as_float(x[mi].e));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int q = 0; q < 32 / (64 / LPR); ++q) {
-      const int r = lane / LPR + q * (64 / LPR);
-      const int64_t i = i0 + wm * 128 + mi * 32 + r;
-      const float2 xs = *reinterpret_cast<const float2*>(ep + r * 132 + 128);
-      const LineScale xr = {xs.x, __float_as_int(xs.y)};
-      float z0[8], z1[8];
+    for (int q = 0; q < 32 / RPL; q += 4) {  // 4 lines of a lane at a time
+      float z0[4][8], z1[GATED ? 4 : 1][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        z0[e] = apply_scale(ep[r * 132 + cl + e], xr, w0[e]) + b0[e];
-        if constexpr (GATED) z1[e] = apply_scale(ep[r * 132 + 64 + cl + e], xr, w1[e]) + b1[e];
+      for (int v = 0; v < 4; ++v) {
+        const float* row = ep + (lane / LPR + (q + v) * RPL) * 132;
+        const float2 xs = *reinterpret_cast<const float2*>(row + 128);
+        const LineScale xr = {xs.x, __float_as_int(xs.y)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          z0[v][e] = apply_scale(row[cl + e], xr, w0[e]) + b0[e];
+          if constexpr (GATED) z1[GATED ? v : 0][e] = apply_scale(row[64 + cl + e], xr, w1[e]) + b1[e];
+        }
       }
-      if (i < p.M && nj > 0) finish8<GATED>(p, i, j, nj, z0, z1);
+      const int64_t i = i0 + wm * 128 + mi * 32 + lane / LPR + q * RPL;
+      if (p.out_dtype == 0) finish_lines<uint16_t, GATED, RPL>(p, i, j, nj, z0, z1);
+      else finish_lines<float, GATED, RPL>(p, i, j, nj, z0, z1);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();

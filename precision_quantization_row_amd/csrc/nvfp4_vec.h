@@ -151,6 +151,19 @@ __device__ __forceinline__ float act_f(int act, float z) {
     default: return z;
   }
 }
+// the activation of 8 values: one branch for all
+__device__ __forceinline__ void act8(int act, float (&z)[8]) {
+  if (act == ACT_GELU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = act_f(ACT_GELU, z[k]);
+  } else if (act == ACT_SILU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = act_f(ACT_SILU, z[k]);
+  } else if (act == ACT_RELU2) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = act_f(ACT_RELU2, z[k]);
+  }
+}
 // d silu / dz = s (1 + z (1 - s)); 1 - s = sigmoid(-z) without cancellation
 __device__ __forceinline__ float dsilu_f(float z, float s) {
   return s * __builtin_fmaf(z, sigmoid_f(-z), 1.0f);
