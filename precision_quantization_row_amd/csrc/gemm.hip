@@ -27,6 +27,7 @@ namespace nvfp4 {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int... I, typename F>
@@ -84,23 +85,23 @@ __device__ __forceinline__ float load_bias(const GemmArgs& p, int64_t j) {
                              : static_cast<const float*>(p.bias)[j];
 }
 // 8 consecutive outputs, from column j on, of each of the lines i, i + STEP,
-// i + 2 STEP, i + 3 STEP; nj columns (8 or more: all) and the lines below M
+// .., i + (NL - 1) STEP; nj columns (8 or more: all) and the lines below M
 // are in the matrix. z0: pre-activations (the gate's, if gated), z1: the up
 // lines'; both with their bias.
-template <typename T, bool GATED, int STEP>
+template <typename T, bool GATED, int NL, int STEP>
 __device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
-                                             float (&z0)[4][8], float (&z1)[GATED ? 4 : 1][8]) {
+                                             float (&z0)[NL][8], float (&z1)[NL][8]) {
   if (nj <= 0) return;
-  Raw8<T> res[4];
+  Raw8<T> res[NL];
   if (p.residual) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < NL; ++v)
       if (i + v * STEP < p.M)
         load8_raw(static_cast<const T*>(p.residual) + (i + v * STEP) * p.N + j, nj, res[v]);
   }
   if (p.z) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < NL; ++v)
       if (i + v * STEP < p.M) {
         T* z = static_cast<T*>(p.z) + (i + v * STEP) * (GATED ? 2 * p.N : p.N) + j;
         store8(z, nj, z0[v]);
@@ -109,16 +110,16 @@ __device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64
   }
   if constexpr (GATED) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < NL; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) z0[v][e] = silu_f(z0[v][e]) * z1[v][e];
   } else if (p.act != ACT_NONE) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) act8(p.act, z0[v]);
+    for (int v = 0; v < NL; ++v) act8(p.act, z0[v]);
   }
   if (p.residual) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < NL; ++v) {
       float r[8];
       unpack8(res[v], r);
 #pragma unroll
@@ -126,7 +127,7 @@ __device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64
     }
   }
 #pragma unroll
-  for (int v = 0; v < 4; ++v)
+  for (int v = 0; v < NL; ++v)
     if (i + v * STEP < p.M) store8(static_cast<T*>(p.y) + (i + v * STEP) * p.N + j, nj, z0[v]);
 }
 
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     for (int q = 0; q < 32 / RPL; q += 4) {  // 4 lines of a lane at a time
-      float z0[4][8], z1[GATED ? 4 : 1][8];
+      float z0[4][8], z1[4][8];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float* row = ep + (lane / LPR + (q + v) * RPL) * 132;
@@ -446,30 +447,230 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           z0[v][e] = apply_scale(row[cl + e], xr, w0[e]) + b0[e];
-          if constexpr (GATED) z1[GATED ? v : 0][e] = apply_scale(row[64 + cl + e], xr, w1[e]) + b1[e];
+          if constexpr (GATED) z1[v][e] = apply_scale(row[64 + cl + e], xr, w1[e]) + b1[e];
         }
       }
       const int64_t i = i0 + wm * 128 + mi * 32 + lane / LPR + q * RPL;
-      if (p.out_dtype == 0) finish_lines<uint16_t, GATED, RPL>(p, i, j, nj, z0, z1);
-      else finish_lines<float, GATED, RPL>(p, i, j, nj, z0, z1);
+      if (p.out_dtype == 0) finish_lines<uint16_t, GATED, 4, RPL>(p, i, j, nj, z0, z1);
+      else finish_lines<float, GATED, 4, RPL>(p, i, j, nj, z0, z1);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
 
+// ---------------------------------------------------------- few-lines kernel
+// For few lines of A (tokens) the product is bound by reading B. A workgroup
+// owns 16 NT lines of B and 16 MT lines of A; its 8 waves split k into runs of
+// whole units, so that a launch of a few hundred workgroups has all of B's
+// bytes on their way at once and no workspace is needed: the waves' sums meet
+// in LDS, in a fixed order. Lines go straight from memory into the lanes that
+// hold them as matrix fragments (lane l: line l % 16, chunk l / 16 of the 64
+// bytes, or 128, that a unit of 128 k takes); PD units are on their way.
+constexpr int RW = 8;  // waves
+template <bool A8, bool GATED, int MT, int NT>
+__global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
+  if (p.noop != nullptr && *p.noop == 1.0f) return;
+  constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT >= 4 ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) float part[RW][MT * 16 * PITCH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
+  const int64_t i0 = (int64_t)blockIdx.y * (16 * MT), j0 = (int64_t)blockIdx.x * (16 * OT);
+  const int K = (int)p.K, qp = (K + 1) / 2, sp = (K + 15) / 16, ap = A8 ? K : qp;
+  const int am = (int)min(p.M - i0, (int64_t)(16 * MT)) - 1, bm = (int)min(p.N - j0, (int64_t)(16 * OT)) - 1;
+  const uint8_t *qa = p.a.q + i0 * ap, *sa = A8 ? nullptr : p.a.s + i0 * sp;
+  const uint8_t *qb = p.b.q + j0 * qp, *sb = p.b.s + j0 * sp;
+  const uint8_t *qu = GATED ? qb + p.N * qp : qb, *su = GATED ? sb + p.N * sp : sb;
+  uint32_t ao[MT], as[MT], bo[NT], bs[NT];  // of this lane's lines, from the tile's first
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int l = min(16 * t + l16, am);
+    ao[t] = (uint32_t)l * ap;
+    as[t] = (uint32_t)l * sp;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int l = min(16 * (GATED ? t % OT : t) + l16, bm);
+    bo[t] = (uint32_t)l * qp;
+    bs[t] = (uint32_t)l * sp;
+  }
+  struct Unit {
+    u32x4 a[MT][A8 ? 2 : 1], b[NT];
+    uint32_t as[A8 ? 1 : MT], bs[NT];
+  } ring[PD];
+  auto fetch = [&](Unit& r, int u) {
+    const int k = 128 * u, c = 32 * g;
+    if (k + 128 <= K) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* q = (GATED && t >= OT ? qu : qb) + k / 2;
+        const uint8_t* s = (GATED && t >= OT ? su : sb) + k / 16;
+        r.b[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a1*>(q + (bo[t] + 16 * g)));
+        r.bs[t] = *reinterpret_cast<const u16_a1*>(s + (bs[t] + 2 * g));
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint8_t* q = qa + (A8 ? k : k / 2);
+        if constexpr (A8) {
+          r.a[t][0] = *reinterpret_cast<const u32x4_a1*>(q + (ao[t] + 32 * g));
+          r.a[t][A8] = *reinterpret_cast<const u32x4_a1*>(q + (ao[t] + 32 * g + 16));
+        } else {
+          r.a[t][0] = *reinterpret_cast<const u32x4_a1*>(q + (ao[t] + 16 * g));
+          r.as[A8 ? 0 : t] = *reinterpret_cast<const u16_a1*>(sa + k / 16 + (as[t] + 2 * g));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint8_t* q = (GATED && t >= OT ? qu : qb) + bo[t];
+        const uint8_t* s = (GATED && t >= OT ? su : sb) + bs[t];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          r.b[t][d] = keep_nibbles(tail_dword(q, qp, (k + c) / 2 + 4 * d), K - k - c - 8 * d);
+        r.bs[t] = keep_bytes(tail_dword(s, sp, (k + c) / 16), sp - (k + c) / 16);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint8_t* q = qa + ao[t];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if constexpr (A8) {
+            r.a[t][0][d] = keep_bytes(tail_dword(q, ap, k + c + 4 * d), K - k - c - 4 * d);
+            r.a[t][A8][d] = keep_bytes(tail_dword(q, ap, k + c + 16 + 4 * d), K - k - c - 16 - 4 * d);
+          } else {
+            r.a[t][0][d] = keep_nibbles(tail_dword(q, qp, (k + c) / 2 + 4 * d), K - k - c - 8 * d);
+          }
+        }
+        if constexpr (!A8)
+          r.as[A8 ? 0 : t] = keep_bytes(tail_dword(sa + as[t], sp, (k + c) / 16), sp - (k + c) / 16);
+      }
+    }
+  };
+  f32x4 acc[MT][NT] = {};
+  auto multiply = [&](const Unit& r) {
+    h2 bsc[NT], asc[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) bsc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.bs[t], 1.0f, false);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      if constexpr (!A8) asc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.as[A8 ? 0 : t], 1.0f, false);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      h8 a[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if constexpr (A8) a[t] = decode8_fp8(r.a[t][d >> 1 ? A8 : 0][(2 * d) & 3], r.a[t][d >> 1 ? A8 : 0][(2 * d + 1) & 3]);
+        else a[t] = decode8_fp4(r.a[t][0][d], d < 2 ? asc[t].xx : asc[t].yy);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const h8 b = decode8_fp4(r.b[n][d], d < 2 ? bsc[n].xx : bsc[n].yy);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a[m], acc[m][n], 0, 0, 0);
+      }
+    }
+  };
+  const int nu = (K + 127) / 128, per = (nu + RW - 1) / RW;
+  const int u0 = wave * per, u1 = min(nu, u0 + per);
+  static_for<PD>([&](auto i) {
+    if (u0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], u0 + decltype(i)::value);
+  });
+#pragma unroll 1
+  for (int u = u0; u < u1; u += PD)
+    static_for<PD>([&](auto i) {
+      constexpr int s = decltype(i)::value;
+      if (u + s < u1) {
+        multiply(ring[s]);
+        if (u + s + PD < u1) fetch(ring[s], u + s + PD);
+      }
+    });
+  // register r of a 16 x 16 result: line l16 of A, line 4 g + r of B
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<f32x4*>(&part[wave][(16 * m + l16) * PITCH + 16 * n + 4 * g]) = acc[m][n];
+  __syncthreads();
+  // 8 consecutive outputs a thread
+  constexpr int LPR = 2 * OT;
+#pragma unroll 1
+  for (int e = tid; e < 16 * MT * LPR; e += RW * 64) {
+    const int r = e / LPR, cl = 8 * (e % LPR);
+    const int64_t i = i0 + r, j = j0 + cl, nj = p.N - j;
+    if (i >= p.M || nj <= 0) continue;
+    float z0[1][8] = {}, z1[1][8] = {};
+#pragma unroll
+    for (int w = 0; w < RW; ++w) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + cl]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) z0[0][x] += q[x / 4][x % 4];
+      if constexpr (GATED) {
+        const f32x4* qg = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + 16 * OT + cl]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) z1[0][x] += qg[x / 4][x % 4];
+      }
+    }
+    const LineScale xs = line_scale(p.a, i);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int64_t jj = min(j + x, p.N - 1);
+      z0[0][x] = apply_scale(z0[0][x], xs, line_scale(p.b, jj)) + load_bias(p, jj);
+      if constexpr (GATED)
+        z1[0][x] = apply_scale(z1[0][x], xs, line_scale(p.b, p.N + jj)) + load_bias(p, p.N + jj);
+    }
+    if (p.out_dtype == 0) finish_lines<uint16_t, GATED, 1, 0>(p, i, j, nj, z0, z1);
+    else finish_lines<float, GATED, 1, 0>(p, i, j, nj, z0, z1);
+  }
+}
+
+template <bool A8, bool GATED, int MT, int NT>
+static void go_rows(const GemmArgs& a, hipStream_t s) {
+  constexpr int OT = GATED ? NT / 2 : NT;
+  const dim3 grid((unsigned)((a.N + 16 * OT - 1) / (16 * OT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((gemm_rows_kernel<A8, GATED, MT, NT>), grid, dim3(RW * 64), 0, s, a);
+}
+
+// Few-lines launch: 16 MT lines of A a workgroup, and the most lines of B that
+// leave at least WG workgroups.
+template <bool A8, bool GATED>
+static void launch_rows(const GemmArgs& a, hipStream_t s) {
+  const int64_t mt = (a.M + 15) / 16;
+  auto groups = [&](int m, int n) {
+    const int ot = GATED ? n / 2 : n;
+    return ((mt + m - 1) / m) * ((a.N + 16 * ot - 1) / (16 * ot));
+  };
+  constexpr int WG = 256;
+  if (mt <= 1) {
+    if (groups(1, 4) >= WG) return go_rows<A8, GATED, 1, 4>(a, s);
+    if (GATED || groups(1, 2) >= WG) return go_rows<A8, GATED, 1, 2>(a, s);
+    return go_rows<A8, GATED, 1, GATED ? 2 : 1>(a, s);
+  }
+  if (mt <= 2) {
+    if (groups(2, 4) >= WG) return go_rows<A8, GATED, 2, 4>(a, s);
+    return go_rows<A8, GATED, 2, 2>(a, s);
+  }
+  if (groups(4, 4) >= WG) return go_rows<A8, GATED, 4, 4>(a, s);
+  return go_rows<A8, GATED, 4, 2>(a, s);
+}
+
 int64_t gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act) {
   const int64_t gm = (M + TM - 1) / TM, gn = (N + TN / 2 - 1) / (TN / 2);
-  if (K > ((int64_t)1 << 28) || gm * gn > ((int64_t)1 << 23)) return -1;
+  if (K > ((int64_t)1 << 23) || N > ((int64_t)1 << 26) || gm * gn > ((int64_t)1 << 23)) return -1;
   return 0;
 }
 
 int launch_gemm(const GemmArgs& a, hipStream_t s) {
-  const bool gated = a.act == ACT_SWIGLU;
+  const bool gated = a.act == ACT_SWIGLU, a8 = a.a.s == nullptr;
+  if (a.M <= 256) {
+    if (a8 && gated) launch_rows<true, true>(a, s);
+    else if (a8) launch_rows<true, false>(a, s);
+    else if (gated) launch_rows<false, true>(a, s);
+    else launch_rows<false, false>(a, s);
+    return hipGetLastError() == hipSuccess ? 0 : -3;
+  }
   const int out = gated ? TN / 2 : TN;
   const int gm = (int)((a.M + TM - 1) / TM), gn = (int)((a.N + out - 1) / out);
   const dim3 grid((unsigned)(gm * gn)), b(256);
-  const bool a8 = a.a.s == nullptr;
   if (a8 && gated) hipLaunchKernelGGL((gemm_tile_kernel<true, true>), grid, b, 0, s, a, gm, gn);
   else if (a8) hipLaunchKernelGGL((gemm_tile_kernel<true, false>), grid, b, 0, s, a, gm, gn);
   else if (gated) hipLaunchKernelGGL((gemm_tile_kernel<false, true>), grid, b, 0, s, a, gm, gn);
