@@ -462,17 +462,67 @@ __global__ void __launch_bounds__(256, 1) gemm_tile_kernel(const GemmArgs p, int
 // ---------------------------------------------------------- few-lines kernel
 // For few lines of A (tokens) the product is bound by reading B. A workgroup
 // owns 16 NT lines of B and 16 MT lines of A; its 8 waves split k into runs of
-// whole units, so that a launch of a few hundred workgroups has all of B's
+// whole quads, so that a launch of a few hundred workgroups has all of B's
 // bytes on their way at once and no workspace is needed: the waves' sums meet
-// in LDS, in a fixed order. Lines go straight from memory into the lanes that
+// in LDS, in a fixed order. Codes go straight from memory into the lanes that
 // hold them as matrix fragments (lane l: line l % 16, chunk l / 16 of the 64
-// bytes, or 128, that a unit of 128 k takes); PD units are on their way.
+// bytes, or 128, that a unit of 128 k takes). A quad is 4 units: a lane would
+// load its block scales 2 bytes at a time, which costs the memory pipe as much
+// as the codes' 16 (3.0 against 4.6 TB/s at 1 x 8192 x 28672 without them), so
+// the wave loads the 32 scale bytes of each line of a quad in whole and hands
+// them out through its own piece of LDS.
 constexpr int RW = 8;  // waves
+
+// The block scales of 16 T lines for one quad, as one wave loads them: 8 bytes
+// a lane (T = 1) or T / 2 times 16.
+template <int T>
+struct QuadScales {
+  static constexpr int PIECES = T == 1 ? 1 : T / 2, DW = T == 1 ? 2 : 4, PER = 8 / DW;
+  uint32_t off[PIECES];  // of this lane's line, from the tile's first
+  bool up[PIECES];       // it is one of the up lines
+  uint32_t w[PIECES][DW];
+  // line(r): offset of the tile's row r; whether it is an up line
+  template <typename F>
+  __device__ __forceinline__ void init(int lane, F line) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) off[i] = line(i * (64 / PER) + lane / PER, up[i]);
+  }
+  __device__ __forceinline__ void load(const uint8_t* s, const uint8_t* su, int lane, int q, int sp) {
+    const int at = 32 * q + 4 * DW * (lane % PER);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const uint8_t* l = (up[i] ? su : s) + off[i];
+      if (32 * (q + 1) <= sp) {
+        if constexpr (DW == 2) {
+          const u32x2 v = *reinterpret_cast<const u32x2_a1*>(l + at);
+          w[i][0] = v.x; w[i][1] = v.y;
+        } else {
+          const u32x4 v = *reinterpret_cast<const u32x4_a1*>(l + at);
+          w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < DW; ++d) w[i][d] = keep_bytes(tail_dword(l, sp, at + 4 * d), sp - at - 4 * d);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(uint8_t* lds, int lane) const {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      uint8_t* d = lds + (i * (64 / PER) + lane / PER) * 32 + 4 * DW * (lane % PER);
+      if constexpr (DW == 2) *reinterpret_cast<u32x2*>(d) = u32x2{w[i][0], w[i][1]};
+      else *reinterpret_cast<u32x4*>(d) = u32x4{w[i][0], w[i][1], w[i][2], w[i][3]};
+    }
+  }
+};
+
 template <bool A8, bool GATED, int MT, int NT>
 __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
-  constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT >= 4 ? 2 : 4;
-  __shared__ __attribute__((aligned(16))) float part[RW][MT * 16 * PITCH];
+  constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT >= 2 ? 2 : NT >= 4 ? 2 : 4;
+  constexpr int SROWS = 16 * (A8 ? NT : NT + MT);  // lines with scales
+  constexpr int PART = RW * MT * 16 * PITCH * 4, SCALES = RW * SROWS * 32;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[PART > SCALES ? PART : SCALES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   const int64_t i0 = (int64_t)blockIdx.y * (16 * MT), j0 = (int64_t)blockIdx.x * (16 * OT);
   const int K = (int)p.K, qp = (K + 1) / 2, sp = (K + 15) / 16, ap = A8 ? K : qp;
@@ -480,33 +530,33 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
   const uint8_t *qa = p.a.q + i0 * ap, *sa = A8 ? nullptr : p.a.s + i0 * sp;
   const uint8_t *qb = p.b.q + j0 * qp, *sb = p.b.s + j0 * sp;
   const uint8_t *qu = GATED ? qb + p.N * qp : qb, *su = GATED ? sb + p.N * sp : sb;
-  uint32_t ao[MT], as[MT], bo[NT], bs[NT];  // of this lane's lines, from the tile's first
+  // this lane's lines, from the tile's first (lines past the matrix repeat its
+  // last one; their products are not stored)
+  uint32_t ao[MT], bo[NT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int l = min(16 * t + l16, am);
-    ao[t] = (uint32_t)l * ap;
-    as[t] = (uint32_t)l * sp;
-  }
+  for (int t = 0; t < MT; ++t) ao[t] = (uint32_t)min(16 * t + l16, am) * ap;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int l = min(16 * (GATED ? t % OT : t) + l16, bm);
-    bo[t] = (uint32_t)l * qp;
-    bs[t] = (uint32_t)l * sp;
-  }
+  for (int t = 0; t < NT; ++t) bo[t] = (uint32_t)min(16 * (t % OT) + l16, bm) * qp;
+  QuadScales<NT> qsb;
+  QuadScales<A8 ? 1 : MT> qsa;
+  qsb.init(lane, [&](int r, bool& up) {
+    up = GATED && r >= 16 * OT;
+    return (uint32_t)min(r % (16 * OT), bm) * sp;
+  });
+  if constexpr (!A8)
+    qsa.init(lane, [&](int r, bool& up) {
+      up = false;
+      return (uint32_t)min(r, am) * sp;
+    });
   struct Unit {
     u32x4 a[MT][A8 ? 2 : 1], b[NT];
-    uint32_t as[A8 ? 1 : MT], bs[NT];
   } ring[PD];
   auto fetch = [&](Unit& r, int u) {
     const int k = 128 * u, c = 32 * g;
     if (k + 128 <= K) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint8_t* q = (GATED && t >= OT ? qu : qb) + k / 2;
-        const uint8_t* s = (GATED && t >= OT ? su : sb) + k / 16;
-        r.b[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a1*>(q + (bo[t] + 16 * g)));
-        r.bs[t] = *reinterpret_cast<const u16_a1*>(s + (bs[t] + 2 * g));
-      }
+      for (int t = 0; t < NT; ++t)
+        r.b[t] = *reinterpret_cast<const u32x4_a1*>((GATED && t >= OT ? qu : qb) + k / 2 + (bo[t] + 16 * g));
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const uint8_t* q = qa + (A8 ? k : k / 2);
@@ -515,18 +565,15 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
           r.a[t][A8] = *reinterpret_cast<const u32x4_a1*>(q + (ao[t] + 32 * g + 16));
         } else {
           r.a[t][0] = *reinterpret_cast<const u32x4_a1*>(q + (ao[t] + 16 * g));
-          r.as[A8 ? 0 : t] = *reinterpret_cast<const u16_a1*>(sa + k / 16 + (as[t] + 2 * g));
         }
       }
     } else {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint8_t* q = (GATED && t >= OT ? qu : qb) + bo[t];
-        const uint8_t* s = (GATED && t >= OT ? su : sb) + bs[t];
 #pragma unroll
         for (int d = 0; d < 4; ++d)
           r.b[t][d] = keep_nibbles(tail_dword(q, qp, (k + c) / 2 + 4 * d), K - k - c - 8 * d);
-        r.bs[t] = keep_bytes(tail_dword(s, sp, (k + c) / 16), sp - (k + c) / 16);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -540,19 +587,22 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
             r.a[t][0][d] = keep_nibbles(tail_dword(q, qp, (k + c) / 2 + 4 * d), K - k - c - 8 * d);
           }
         }
-        if constexpr (!A8)
-          r.as[A8 ? 0 : t] = keep_bytes(tail_dword(sa + as[t], sp, (k + c) / 16), sp - (k + c) / 16);
       }
     }
   };
   f32x4 acc[MT][NT] = {};
-  auto multiply = [&](const Unit& r) {
+  uint8_t* ls = lds + wave * SROWS * 32;  // B's scales, then A's
+  auto multiply = [&](const Unit& r, int u) {  // u: unit of its quad
     h2 bsc[NT], asc[MT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) bsc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.bs[t], 1.0f, false);
+    for (int t = 0; t < NT; ++t)
+      bsc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(
+          *reinterpret_cast<const uint16_t*>(ls + (16 * t + l16) * 32 + 8 * u + 2 * g), 1.0f, false);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-      if constexpr (!A8) asc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.as[A8 ? 0 : t], 1.0f, false);
+      if constexpr (!A8)
+        asc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(
+            *reinterpret_cast<const uint16_t*>(ls + (16 * (NT + t) + l16) * 32 + 8 * u + 2 * g), 1.0f, false);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       h8 a[MT];
@@ -570,20 +620,37 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
       }
     }
   };
-  const int nu = (K + 127) / 128, per = (nu + RW - 1) / RW;
-  const int u0 = wave * per, u1 = min(nu, u0 + per);
+  const int nu = (K + 127) / 128, nq = (nu + 3) / 4, per = (nq + RW - 1) / RW;
+  const int q0 = wave * per, u1 = min(nu, 4 * (q0 + per));
+  if (4 * q0 < u1) {
+    qsb.load(sb, su, lane, q0, sp);
+    if constexpr (!A8) qsa.load(sa, sa, lane, q0, sp);
+  }
   static_for<PD>([&](auto i) {
-    if (u0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], u0 + decltype(i)::value);
+    if (4 * q0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], 4 * q0 + decltype(i)::value);
   });
 #pragma unroll 1
-  for (int u = u0; u < u1; u += PD)
-    static_for<PD>([&](auto i) {
+  for (int q = q0; 4 * q < u1; ++q) {
+    // (a wave's LDS accesses are done in order: the last quad's reads precede)
+    qsb.put(ls, lane);
+    if constexpr (!A8) qsa.put(ls + NT * 512, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (4 * (q + 1) < u1) {
+      qsb.load(sb, su, lane, q + 1, sp);
+      if constexpr (!A8) qsa.load(sa, sa, lane, q + 1, sp);
+    }
+    static_for<4>([&](auto i) {
       constexpr int s = decltype(i)::value;
-      if (u + s < u1) {
-        multiply(ring[s]);
-        if (u + s + PD < u1) fetch(ring[s], u + s + PD);
+      const int u = 4 * q + s;
+      if (u < u1) {
+        multiply(ring[s % PD], s);
+        if (u + PD < u1) fetch(ring[s % PD], u + PD);
       }
     });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __syncthreads();  // the scales' LDS becomes the sums'
+  float(*part)[MT * 16 * PITCH] = reinterpret_cast<float(*)[MT * 16 * PITCH]>(lds);
   // register r of a 16 x 16 result: line l16 of A, line 4 g + r of B
 #pragma unroll
   for (int m = 0; m < MT; ++m)
