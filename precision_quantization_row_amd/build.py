@@ -2,8 +2,8 @@
 the reference streaming kernels bench.py measures the HBM ceiling with
 (bench_ref/libstream_ref.so, not part of the library).
 
-hipcc compiles every .hip source under csrc/ into one shared library next to
-this file. Flags:
+hipcc compiles every .hip source under csrc/ (several at a time) into one
+shared library next to this file. Flags:
   --offload-arch=gfx950                 CDNA4 only, no other targets
   -O3 -ffp-contract=off                 no fused multiply-add contraction, so
                                         every product / quotient is rounded once
@@ -16,6 +16,8 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -40,13 +42,20 @@ def stream_ref_path() -> str:
 def _hipcc(sources, out, includes, verbose):
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = out + ".tmp"
-    cmd = [hipcc, *FLAGS]
-    for inc in includes:
-        cmd += ["-I", inc]
-    cmd += [*sources, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    inc = [x for i in includes for x in ("-I", i)]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, f"{i}.o") for i in range(len(sources))]
+        jobs = [[hipcc, *(f for f in FLAGS if f != "-shared"), *inc, "-c", s, "-o", o]
+                for s, o in zip(sources, objs)]
+        with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+            list(pool.map(run, jobs))
+        run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", tmp])
     os.replace(tmp, out)
     return out
 

@@ -1,0 +1,279 @@
+// gemm_rows.hip -- the packed product for few lines of A (gfx950).
+#include "gemm_device.h"
+
+namespace nvfp4 {
+
+// ---------------------------------------------------------- few-lines kernel
+// For few lines of A (tokens) the product is bound by reading B. A workgroup
+// owns 16 NT lines of B and 16 MT lines of A; its 8 waves split k into runs of
+// whole quads, so that a launch of a few hundred workgroups has all of B's
+// bytes on their way at once and no workspace is needed: the waves' sums meet
+// in LDS, in a fixed order. Codes go straight from memory into the lanes that
+// hold them as matrix fragments (lane l: line l % 16, chunk l / 16 of the 64
+// bytes, or 128, that a unit of 128 k takes). A quad is 4 units: a lane would
+// load its block scales 2 bytes at a time, which costs the memory pipe as much
+// as the codes' 16 (3.0 against 4.6 TB/s at 1 x 8192 x 28672 without them), so
+// the wave loads the 32 scale bytes of each line of a quad in whole and hands
+// them out through its own piece of LDS.
+
+// The block scales of 16 T lines for one quad, as one wave loads them: 8 bytes
+// a lane (T = 1) or T / 2 times 16.
+constexpr int RW = 8;  // waves
+
+template <int T>
+struct QuadScales {
+  static constexpr int PIECES = T == 1 ? 1 : T / 2, DW = T == 1 ? 2 : 4, PER = 8 / DW;
+  uint32_t off[PIECES];  // of this lane's line, from the tile's first
+  bool up[PIECES];       // it is one of the up lines
+  uint32_t w[2][PIECES][DW];  // of even and odd quads
+  // line(r): offset of the tile's row r; whether it is an up line
+  template <typename F>
+  __device__ __forceinline__ void init(int lane, F line) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) off[i] = line(i * (64 / PER) + lane / PER, up[i]);
+  }
+  template <int H>
+  __device__ __forceinline__ void load(const uint8_t* s, const uint8_t* su, int lane, int q, int sp) {
+    const int at = 32 * q + 4 * DW * (lane % PER);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const uint8_t* l = (up[i] ? su : s) + off[i];
+      if (32 * (q + 1) <= sp) {
+        if constexpr (DW == 2) {
+          const u32x2 v = *reinterpret_cast<const u32x2_a1*>(l + at);
+          w[H][i][0] = v.x; w[H][i][1] = v.y;
+        } else {
+          const u32x4 v = *reinterpret_cast<const u32x4_a1*>(l + at);
+          w[H][i][0] = v.x; w[H][i][1] = v.y; w[H][i][2] = v.z; w[H][i][3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < DW; ++d) w[H][i][d] = keep_bytes(tail_dword(l, sp, at + 4 * d), sp - at - 4 * d);
+      }
+    }
+  }
+  template <int H>
+  __device__ __forceinline__ void put(uint8_t* lds, int lane) const {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      uint8_t* d = lds + (i * (64 / PER) + lane / PER) * 32 + 4 * DW * (lane % PER);
+      if constexpr (DW == 2) *reinterpret_cast<u32x2*>(d) = u32x2{w[H][i][0], w[H][i][1]};
+      else *reinterpret_cast<u32x4*>(d) = u32x4{w[H][i][0], w[H][i][1], w[H][i][2], w[H][i][3]};
+    }
+  }
+};
+
+template <bool A8, bool GATED, int MT, int NT>
+__global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
+  if (p.noop != nullptr && *p.noop == 1.0f) return;
+  constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT == 1 ? 4 : 2;
+  constexpr int SROWS = 16 * (A8 ? NT : NT + MT);  // lines with scales
+  constexpr int PART = RW * MT * 16 * PITCH * 4, SCALES = RW * SROWS * 32;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[PART > SCALES ? PART : SCALES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
+  const int64_t i0 = (int64_t)blockIdx.y * (16 * MT), j0 = (int64_t)blockIdx.x * (16 * OT);
+  const int K = (int)p.K, qp = (K + 1) / 2, sp = (K + 15) / 16, ap = A8 ? K : qp;
+  const int am = (int)min(p.M - i0, (int64_t)(16 * MT)) - 1, bm = (int)min(p.N - j0, (int64_t)(16 * OT)) - 1;
+  const uint8_t *qa = p.a.q + i0 * ap, *sa = A8 ? nullptr : p.a.s + i0 * sp;
+  const uint8_t *qb = p.b.q + j0 * qp, *sb = p.b.s + j0 * sp;
+  const uint8_t *qu = GATED ? qb + p.N * qp : qb, *su = GATED ? sb + p.N * sp : sb;
+  // this lane's lines, from the tile's first (lines past the matrix repeat its
+  // last one; their products are not stored)
+  uint32_t ao[MT], bo[NT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) ao[t] = (uint32_t)min(16 * t + l16, am) * ap + (A8 ? 32 : 16) * g;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) bo[t] = (uint32_t)min(16 * (t % OT) + l16, bm) * qp + 16 * g;
+  QuadScales<NT> qsb;
+  QuadScales<A8 ? 1 : MT> qsa;
+  qsb.init(lane, [&](int r, bool& up) {
+    up = GATED && r >= 16 * OT;
+    return (uint32_t)min(r % (16 * OT), bm) * sp;
+  });
+  if constexpr (!A8)
+    qsa.init(lane, [&](int r, bool& up) {
+      up = false;
+      return (uint32_t)min(r, am) * sp;
+    });
+  struct Unit {
+    u32x4 a[MT][A8 ? 2 : 1], b[NT];
+  } ring[PD];
+  // Unit u; past the lines' end zeros. (The offsets include 16 g, 32 g.)
+  auto fetch = [&](Unit& r, int u) __attribute__((always_inline)) {
+    const int k = 128 * u;
+    if (k + 128 <= K) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        r.b[t] = *reinterpret_cast<const u32x4_a1*>((GATED && t >= OT ? qu : qb) + k / 2 + bo[t]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint8_t* q = qa + (A8 ? k : k / 2);
+        r.a[t][0] = *reinterpret_cast<const u32x4_a1*>(q + ao[t]);
+        if constexpr (A8) r.a[t][A8] = *reinterpret_cast<const u32x4_a1*>(q + 16 + ao[t]);
+      }
+    } else {
+      const int kc = k + 32 * g;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          r.b[t][d] = keep_nibbles(
+              tail_dword((GATED && t >= OT ? qu : qb) + bo[t] - 16 * g, qp, kc / 2 + 4 * d), K - kc - 8 * d);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const uint8_t* q = qa + ao[t] - (A8 ? 32 : 16) * g;
+          if constexpr (A8) {
+            r.a[t][0][d] = keep_bytes(tail_dword(q, ap, kc + 4 * d), K - kc - 4 * d);
+            r.a[t][A8][d] = keep_bytes(tail_dword(q, ap, kc + 16 + 4 * d), K - kc - 16 - 4 * d);
+          } else {
+            r.a[t][0][d] = keep_nibbles(tail_dword(q, qp, kc / 2 + 4 * d), K - kc - 8 * d);
+          }
+        }
+      }
+    }
+  };
+  f32x4 acc[MT][NT] = {};
+  uint8_t* ls = lds + wave * SROWS * 32;  // B's scales, then A's
+  auto multiply = [&](const Unit& r, int u) __attribute__((always_inline)) {  // u: unit of its quad
+    h2 bsc[NT], asc[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      bsc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(
+          *reinterpret_cast<const uint16_t*>(ls + (16 * t + l16) * 32 + 8 * u + 2 * g), 1.0f, false);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      if constexpr (!A8)
+        asc[t] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(
+            *reinterpret_cast<const uint16_t*>(ls + (16 * (NT + t) + l16) * 32 + 8 * u + 2 * g), 1.0f, false);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      h8 a[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if constexpr (A8) a[t] = decode8_fp8(r.a[t][d >> 1 ? A8 : 0][(2 * d) & 3], r.a[t][d >> 1 ? A8 : 0][(2 * d + 1) & 3]);
+        else a[t] = decode8_fp4(r.a[t][0][d], d < 2 ? asc[t].xx : asc[t].yy);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const h8 b = decode8_fp4(r.b[n][d], d < 2 ? bsc[n].xx : bsc[n].yy);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a[m], acc[m][n], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (decoded ahead, fragments would cost waves)
+    }
+  };
+  const int nu = (K + 127) / 128, nq = (nu + 3) / 4, per = (nq + RW - 1) / RW;
+  const int q0 = wave * per, u1 = min(nu, 4 * (q0 + per));
+  static_for<2>([&](auto i) __attribute__((always_inline)) {
+    constexpr int h = decltype(i)::value;
+    if (4 * (q0 + h) < u1) {
+      qsb.template load<h>(sb, su, lane, q0 + h, sp);
+      if constexpr (!A8) qsa.template load<h>(sa, sa, lane, q0 + h, sp);
+    }
+  });
+  static_for<PD>([&](auto i) __attribute__((always_inline)) {
+    if (4 * q0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], 4 * q0 + decltype(i)::value);
+  });
+#pragma unroll 1
+  for (int q2 = q0; 4 * q2 < u1; q2 += 2)
+    static_for<2>([&](auto h_) __attribute__((always_inline)) {
+      constexpr int h = decltype(h_)::value;
+      const int q = q2 + h;
+      if (4 * q < u1) {
+        // (a wave's LDS accesses are done in order: the last quad's reads precede)
+        qsb.template put<h>(ls, lane);
+        if constexpr (!A8) qsa.template put<h>(ls + NT * 512, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (4 * (q + 2) < u1) {
+          qsb.template load<h>(sb, su, lane, q + 2, sp);
+          if constexpr (!A8) qsa.template load<h>(sa, sa, lane, q + 2, sp);
+        }
+        static_for<4>([&](auto i) __attribute__((always_inline)) {
+          constexpr int s = decltype(i)::value, r = (4 * h + s) % PD;
+          const int u = 4 * q + s;
+          if (u < u1) {
+            multiply(ring[r], s);
+            if (u + PD < u1) fetch(ring[r], u + PD);
+          }
+        });
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+    });
+  __syncthreads();  // the scales' LDS becomes the sums'
+  float(*part)[MT * 16 * PITCH] = reinterpret_cast<float(*)[MT * 16 * PITCH]>(lds);
+  // register r of a 16 x 16 result: line l16 of A, line 4 g + r of B
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<f32x4*>(&part[wave][(16 * m + l16) * PITCH + 16 * n + 4 * g]) = acc[m][n];
+  __syncthreads();
+  // 8 consecutive outputs a thread
+  constexpr int LPR = 2 * OT;
+#pragma unroll 1
+  for (int e = tid; e < 16 * MT * LPR; e += RW * 64) {
+    const int r = e / LPR, cl = 8 * (e % LPR);
+    const int64_t i = i0 + r, j = j0 + cl, nj = p.N - j;
+    if (i >= p.M || nj <= 0) continue;
+    float z0[1][8] = {}, z1[1][8] = {};
+#pragma unroll 2  // (more sums in flight would cost the main loop its waves)
+    for (int w = 0; w < RW; ++w) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + cl]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) z0[0][x] += q[x / 4][x % 4];
+      if constexpr (GATED) {
+        const f32x4* qg = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + 16 * OT + cl]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) z1[0][x] += qg[x / 4][x % 4];
+      }
+    }
+    const LineScale xs = line_scale(p.a, i);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int64_t jj = min(j + x, p.N - 1);
+      z0[0][x] = apply_scale(z0[0][x], xs, line_scale(p.b, jj)) + load_bias(p, jj);
+      if constexpr (GATED)
+        z1[0][x] = apply_scale(z1[0][x], xs, line_scale(p.b, p.N + jj)) + load_bias(p, p.N + jj);
+    }
+    if (p.out_dtype == 0) finish_lines<uint16_t, GATED, 1, 0>(p, i, j, nj, z0, z1);
+    else finish_lines<float, GATED, 1, 0>(p, i, j, nj, z0, z1);
+  }
+}
+
+template <bool A8, bool GATED, int MT, int NT>
+static void go_rows(const GemmArgs& a, hipStream_t s) {
+  constexpr int OT = GATED ? NT / 2 : NT;
+  const dim3 grid((unsigned)((a.N + 16 * OT - 1) / (16 * OT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((gemm_rows_kernel<A8, GATED, MT, NT>), grid, dim3(RW * 64), 0, s, a);
+}
+
+// The tile of a few-lines launch: the widest one that leaves a workgroup for
+// each of the 256 CUs. (1 x 57344 x 8192: NT 2 with 4 units on their way 54 us,
+// NT 4 with 2 64 us, NT 4 with 4 73 us: the registers cost it the second
+// workgroup of a CU.)
+template <bool A8, bool GATED>
+static void launch_rows_t(const GemmArgs& a, hipStream_t s) {
+  const int64_t mt = (a.M + 15) / 16;
+  auto groups = [&](int m, int n) {
+    const int ot = GATED ? n / 2 : n;
+    return ((mt + m - 1) / m) * ((a.N + 16 * ot - 1) / (16 * ot));
+  };
+  if (mt <= 1) {
+    if (GATED || groups(1, 2) >= 256) return go_rows<A8, GATED, 1, 2>(a, s);
+    return go_rows<A8, GATED, 1, GATED ? 2 : 1>(a, s);
+  }
+  if (mt <= 2) return go_rows<A8, GATED, 2, 2>(a, s);
+  if (groups(4, 4) >= 256) return go_rows<A8, GATED, 4, 4>(a, s);
+  return go_rows<A8, GATED, 4, 2>(a, s);
+}
+
+void launch_gemm_rows(const GemmArgs& a, hipStream_t s) {
+  const bool gated = a.act == ACT_SWIGLU, a8 = a.a.s == nullptr;
+  if (a8 && gated) launch_rows_t<true, true>(a, s);
+  else if (a8) launch_rows_t<true, false>(a, s);
+  else if (gated) launch_rows_t<false, true>(a, s);
+  else launch_rows_t<false, false>(a, s);
+}
+
+}  // namespace nvfp4

@@ -150,5 +150,8 @@ struct GemmArgs {
 };
 int64_t gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act);
 int launch_gemm(const GemmArgs& a, hipStream_t s);
+int64_t gemm_tiles(int64_t M, int64_t N, bool gated);  // workgroups of the tile kernel
+void launch_gemm_tile(const GemmArgs& a, hipStream_t s);
+void launch_gemm_rows(const GemmArgs& a, hipStream_t s);
 
 }  // namespace nvfp4
