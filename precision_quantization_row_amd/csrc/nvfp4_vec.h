@@ -49,12 +49,13 @@ __device__ __forceinline__ void load8_raw(const uint16_t* p, int64_t n, Raw8<uin
     }
   }
 }
+// (FP32: a lane's run is two accesses, each half of a wave's 2 KB; past the
+// caches, NT, the halves would move on their own)
 template <bool NT = false>
 __device__ __forceinline__ void load8_raw(const float* p, int64_t n, Raw8<float>& r) {
   if (n >= 8) {
     const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(p);
-    const u32x4 a = NT ? __builtin_nontemporal_load(q) : q[0];
-    const u32x4 b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+    const u32x4 a = q[0], b = q[1];
     r.d[0] = a.x; r.d[1] = a.y; r.d[2] = a.z; r.d[3] = a.w;
     r.d[4] = b.x; r.d[5] = b.y; r.d[6] = b.z; r.d[7] = b.w;
   } else {
@@ -103,13 +104,8 @@ __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8])
     const u32x4 b = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
                      __float_as_uint(v[7])};
     u32x4_a4* q = reinterpret_cast<u32x4_a4*>(p);
-    if (NT) {
-      __builtin_nontemporal_store(a, q);
-      __builtin_nontemporal_store(b, q + 1);
-    } else {
-      q[0] = a;
-      q[1] = b;
-    }
+    q[0] = a;
+    q[1] = b;
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
