@@ -311,20 +311,14 @@ int nvfp4_quantize_dequantize(const void* x, int in_dtype, int64_t M, int64_t K,
  *   z       [M][N] ([M][2 N] for ACT_SWIGLU) of out_dtype, or NULL: the value
  *           before the activation, for nvfp4_act_backward
  *   y       [M][N] of out_dtype (NVFP4_BF16 or NVFP4_FP32)
- *   workspace: device memory of at least nvfp4_gemm_workspace bytes, 16-byte
- *           aligned (NULL where that is 0); contents are scratch
- * M, N, K >= 1, any values and any alignment of the operands. Tensors with
- * more than 2^31 - 1 tiles of the kernel's grid are NVFP4_ERR_UNSUPPORTED. */
+ * M, N, K >= 1, any values and any alignment of the operands. K above 2^23,
+ * N above 2^26 and products of more than 2^23 tiles of 256 x 256 are
+ * NVFP4_ERR_UNSUPPORTED. No workspace is needed. */
 int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, const float* a_amax,
                float a_bound, const uint8_t* b, const uint8_t* b_scale, int b_mode,
                const float* b_amax, float b_bound, int64_t M, int64_t N, int64_t K,
                const void* bias, int bias_dtype, int act, const void* residual, void* z, void* y,
-               int out_dtype, void* workspace, int64_t workspace_bytes, const float* noop,
-               void* stream);
-
-/* Workspace bytes nvfp4_gemm needs for these arguments (host-only; 0 for bad
- * arguments, which nvfp4_gemm itself rejects). */
-int64_t nvfp4_gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act);
+               int out_dtype, const float* noop, void* stream);
 
 /* Backward pass of nvfp4_gemm's epilogue:
  *   dz_ij   = dy_ij act'(z_ij);  ACT_SWIGLU, z = [g | u]:

@@ -54,7 +54,7 @@ EXPORTED = ("nvfp4_amax_path", "nvfp4_amax_rowcol", "nvfp4_group_amax_expand",
             "nvfp4_quantize_2d",
             "nvfp4_quantize_grouped",
             "nvfp4_quantize_dequantize", "nvfp4_dequantize",
-            "nvfp4_gemm", "nvfp4_gemm_workspace",
+            "nvfp4_gemm",
             "nvfp4_act_backward", "nvfp4_act_backward_workspace",
             "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace",
             "nvfp4_status_string")
@@ -113,9 +113,7 @@ def load_library():
     lib.nvfp4_dequantize.argtypes = [u8p, u8p, i64, i64, c_int, f32p, c_f, vp, c_int, f32p, vp]
     lib.nvfp4_gemm.restype = c_int
     lib.nvfp4_gemm.argtypes = [c_int, u8p, u8p, c_int, f32p, c_f, u8p, u8p, c_int, f32p, c_f,
-                               i64, i64, i64, vp, c_int, c_int, vp, vp, vp, c_int, vp, i64, f32p, vp]
-    lib.nvfp4_gemm_workspace.restype = i64
-    lib.nvfp4_gemm_workspace.argtypes = [c_int, i64, i64, i64, c_int]
+                               i64, i64, i64, vp, c_int, c_int, vp, vp, vp, c_int, f32p, vp]
     lib.nvfp4_act_backward.restype = c_int
     lib.nvfp4_act_backward.argtypes = [vp, vp, c_int, i64, i64, c_int, vp, f32p, vp, i64, f32p, vp]
     lib.nvfp4_act_backward_workspace.restype = i64
@@ -429,10 +427,13 @@ def _arg(t, name: str, dtypes, numel: int, dev) -> Optional[int]:
     """The device address of an optional tensor argument, checked."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype not in dtypes or t.numel() != numel or t.device != dev or not t.is_contiguous():
-        _dev(t, name, dtypes, numel, dev)
+    try:
+        if (t.dtype in dtypes and t.numel() == numel and t.get_device() == dev.index
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtypes, numel, dev)
     return t.data_ptr()
 
 
@@ -470,26 +471,18 @@ def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
     return ws, ws.data_ptr(), size
 
 
-def nvfp4_gemm_workspace(a_fmt: int, M: int, N: int, K: int, act: int = NVFP4_ACT_NONE) -> int:
-    """Workspace bytes of nvfp4_gemm."""
-    return load_library().nvfp4_gemm_workspace(a_fmt, M, N, K, act)
-
-
 def nvfp4_gemm(a: torch.Tensor, a_scale: Optional[torch.Tensor], a_mode: int, a_amax: torch.Tensor,
                a_bound: float, b: torch.Tensor, b_scale: torch.Tensor, b_mode: int,
                b_amax: torch.Tensor, b_bound: float, M: int, N: int, K: int, y: torch.Tensor,
                bias: Optional[torch.Tensor] = None, act: int = NVFP4_ACT_NONE,
                residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
-               workspace: Optional[torch.Tensor] = None, noop: Optional[torch.Tensor] = None,
-               stream=None) -> None:
+               noop: Optional[torch.Tensor] = None, stream=None) -> None:
     """y [M, N] = act(A B^T + bias) + residual of packed operands.
 
     a: uint8 codes [M, ceil(K/2)] with a_scale [M, ceil(K/16)] (NVFP4), or
     float8_e4m3fn [M, K] with a_scale None (8-bit lines). b: the N lines (2 N
     for NVFP4_ACT_SWIGLU: gate lines, then up lines), NVFP4. y, z and residual
-    share y's dtype (bfloat16 or float32); bias is bfloat16 or float32. A
-    workspace, where the sizes need one (nvfp4_gemm_workspace), is taken from
-    torch's allocator unless given."""
+    share y's dtype (bfloat16 or float32); bias is bfloat16 or float32."""
     lib = _lib or load_library()
     dev = _first(a, "a", (torch.uint8, torch.float8_e4m3fn))
     fmt = NVFP4_FMT_NVFP4 if a.dtype == torch.uint8 else NVFP4_FMT_E4M3
@@ -503,8 +496,6 @@ def nvfp4_gemm(a: torch.Tensor, a_scale: Optional[torch.Tensor], a_mode: int, a_
     NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
     kq, ks = (K + 1) // 2, (K + 15) // 16
     same = (y.dtype,)
-    need = lib.nvfp4_gemm_workspace(fmt, M, N, K, act)
-    ws, wp, wb = _workspace(workspace, need, dev, stream) if need > 0 else (None, None, 0)
     st = lib.nvfp4_gemm(
         fmt, _arg(a, "a", (a.dtype,), M * (kq if fmt == NVFP4_FMT_NVFP4 else K), dev),
         _arg(a_scale, "a_scale", _SCALE_DTYPES, M * ks, dev), a_mode,
@@ -514,7 +505,7 @@ def nvfp4_gemm(a: torch.Tensor, a_scale: Optional[torch.Tensor], a_mode: int, a_
         M, N, K, _arg(bias, "bias", _OUT_CODES, NB, dev),
         0 if bias is None else _OUT_CODES[bias.dtype], act,
         _arg(residual, "residual", same, M * N, dev), _arg(z, "z", same, M * NB, dev),
-        _arg(y, "y", same, M * N, dev), out, wp, wb, _arg(noop, "noop", _F32, 1, dev),
+        _arg(y, "y", same, M * N, dev), out, _arg(noop, "noop", _F32, 1, dev),
         _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_gemm", st)

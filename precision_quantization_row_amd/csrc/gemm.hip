@@ -3,11 +3,10 @@
 
 namespace nvfp4 {
 
-int64_t gemm_workspace(int, int64_t M, int64_t N, int64_t K, int act) {
-  if (K > ((int64_t)1 << 23) || N > ((int64_t)1 << 26) ||
-      gemm_tiles(M, N, act == 4) > ((int64_t)1 << 23))
-    return -1;
-  return 0;
+// What 32-bit offsets within a tile and the launch grids hold.
+bool gemm_supported(int64_t M, int64_t N, int64_t K, bool gated) {
+  return K <= ((int64_t)1 << 23) && N <= ((int64_t)1 << 26) &&
+         M <= ((int64_t)1 << 31) && gemm_tiles(M, N, gated) <= ((int64_t)1 << 23);
 }
 
 // Both kernels take any sizes; the quicker one runs. The few-lines kernel does
@@ -18,6 +17,9 @@ int64_t gemm_workspace(int, int64_t M, int64_t N, int64_t K, int act) {
 static bool few_lines(const GemmArgs& a) {
   const bool gated = a.act == 4;
   const double lines = (double)((a.M + 63) / 64 * 64), nb = (double)(gated ? 2 * a.N : a.N), K = (double)a.K;
+  // a launch holds fewer than 2^32 threads; the few-lines kernel's tiles are
+  // at least 64 (or all) lines by 16 outputs and have 512
+  if ((lines / 64) * (nb / 16 + 1) > (double)(1 << 22)) return false;
   const double rounds = (double)((gemm_tiles(a.M, a.N, gated) + 255) / 256);
   return lines * nb * K < rounds * (6.4e6 * K + 4.2e9);
 }

@@ -64,14 +64,14 @@ struct QuadScales {
 };
 
 template <bool A8, bool GATED, int MT, int NT>
-__global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
+__global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p, unsigned gn) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
   constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT == 1 ? 4 : 2;
   constexpr int SROWS = 16 * (A8 ? NT : NT + MT);  // lines with scales
   constexpr int PART = RW * MT * 16 * PITCH * 4, SCALES = RW * SROWS * 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds[PART > SCALES ? PART : SCALES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
-  const int64_t i0 = (int64_t)blockIdx.y * (16 * MT), j0 = (int64_t)blockIdx.x * (16 * OT);
+  const int64_t i0 = (int64_t)(blockIdx.x / gn) * (16 * MT), j0 = (int64_t)(blockIdx.x % gn) * (16 * OT);
   const int K = (int)p.K, qp = (K + 1) / 2, sp = (K + 15) / 16, ap = A8 ? K : qp;
   const int am = (int)min(p.M - i0, (int64_t)(16 * MT)) - 1, bm = (int)min(p.N - j0, (int64_t)(16 * OT)) - 1;
   const uint8_t *qa = p.a.q + i0 * ap, *sa = A8 ? nullptr : p.a.s + i0 * sp;
@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p) {
 template <bool A8, bool GATED, int MT, int NT>
 static void go_rows(const GemmArgs& a, hipStream_t s) {
   constexpr int OT = GATED ? NT / 2 : NT;
-  const dim3 grid((unsigned)((a.N + 16 * OT - 1) / (16 * OT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((gemm_rows_kernel<A8, GATED, MT, NT>), grid, dim3(RW * 64), 0, s, a);
+  const unsigned gn = (unsigned)((a.N + 16 * OT - 1) / (16 * OT));
+  const unsigned gm = (unsigned)((a.M + 16 * MT - 1) / (16 * MT));  // (few_lines bounds gm gn)
+  hipLaunchKernelGGL((gemm_rows_kernel<A8, GATED, MT, NT>), dim3(gm * gn), dim3(RW * 64), 0, s, a, gn);
 }
 
 // The tile of a few-lines launch: the widest one that leaves a workgroup for

@@ -315,18 +315,11 @@ static bool valid_dtype(int d) { return d == NVFP4_BF16 || d == NVFP4_FP32; }
 constexpr int64_t kMaxSize = (int64_t)1 << 40;   // beyond: an argument error
 constexpr int64_t kMaxCols = (int64_t)1 << 27;   // of the row-wise kernels
 
-int64_t nvfp4_gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act) {
-  if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return 0;
-  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return 0;
-  return gemm_workspace(a_fmt, M, N, K, act);
-}
-
 int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, const float* a_amax,
                float a_bound, const uint8_t* b, const uint8_t* b_scale, int b_mode,
                const float* b_amax, float b_bound, int64_t M, int64_t N, int64_t K,
                const void* bias, int bias_dtype, int act, const void* residual, void* z, void* y,
-               int out_dtype, void* workspace, int64_t workspace_bytes, const float* noop,
-               void* stream) {
+               int out_dtype, const float* noop, void* stream) {
   if (!a || !a_amax || !b || !b_scale || !b_amax || !y) return NVFP4_ERR_ARG;
   if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
   if (a_fmt != NVFP4_FMT_NVFP4 && a_fmt != NVFP4_FMT_E4M3) return NVFP4_ERR_ARG;
@@ -338,11 +331,7 @@ int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, 
   if (!valid_bound(b_bound)) return NVFP4_ERR_ARG;
   if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return NVFP4_ERR_ARG;
   if (!valid_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype))) return NVFP4_ERR_ARG;
-  const int64_t need = gemm_workspace(a_fmt, M, N, K, act);
-  if (need < 0) return NVFP4_ERR_UNSUPPORTED;
-  if (need > 0 && (!workspace || workspace_bytes < need ||
-                   (reinterpret_cast<uintptr_t>(workspace) & 15) != 0))
-    return NVFP4_ERR_ARG;
+  if (!gemm_supported(M, N, K, act == NVFP4_ACT_SWIGLU)) return NVFP4_ERR_UNSUPPORTED;
   GemmArgs g;
   g.a = {a, a_scale, a_amax, a_mode,
          a_fmt == NVFP4_FMT_E4M3 ? 1.0f / 448.0f : 1.0f / (a_bound * 6.0f)};
@@ -357,7 +346,6 @@ int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, 
   g.z = z;
   g.y = y;
   g.out_dtype = out_dtype;
-  g.ws = static_cast<float*>(workspace);
   g.noop = noop;
   return launch_gemm(g, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
 }

@@ -145,10 +145,9 @@ struct GemmArgs {
   void* z;
   void* y;
   int out_dtype;      // of y, z and residual
-  float* ws;
   const float* noop;
 };
-int64_t gemm_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int act);
+bool gemm_supported(int64_t M, int64_t N, int64_t K, bool gated);
 int launch_gemm(const GemmArgs& a, hipStream_t s);
 int64_t gemm_tiles(int64_t M, int64_t N, bool gated);  // workgroups of the tile kernel
 void launch_gemm_tile(const GemmArgs& a, hipStream_t s);

@@ -266,9 +266,7 @@ def test_replays_in_a_graph():
         a, sa, aa = sets[0][0].dev()
         b, sb, ab = sets[0][1].dev()
         y = torch.empty(M, N, device=DEV)
-        need = p.nvfp4_gemm_workspace(p.NVFP4_FMT_NVFP4, M, N, K)
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
-        call = lambda: p.nvfp4_gemm(a, sa, 1, aa, 448.0, b, sb, 1, ab, 448.0, M, N, K, y, workspace=ws)
+        call = lambda: p.nvfp4_gemm(a, sa, 1, aa, 448.0, b, sb, 1, ab, 448.0, M, N, K, y)
         call()
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()

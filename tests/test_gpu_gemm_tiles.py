@@ -138,6 +138,17 @@ def test_address_residual_in_place_and_noop():
         assert torch.equal(acc, sum_)
 
 
+@pytest.mark.parametrize("M,N,K", [(4500000, 2, 16), (70000, 70, 33)])
+def test_very_many_lines(M, N, K):
+    """More workgroups along the lines than a grid's second axis holds."""
+    say(f"[gpu] gemm tall {M}x{N}x{K}")
+    rng = np.random.RandomState(9)
+    A, B = random_lines(rng, M, K, exact=True), random_lines(rng, N, K, exact=True)
+    y, _ = run(A, B, N)
+    want, big = exact_z(A, B)
+    assert torch.equal(y.double()[big], want[big])
+
+
 def test_garbage_outside_odd_lines():
     M, N, K = 5000, 5001, 255
     rng = np.random.RandomState(4)
