@@ -9,19 +9,20 @@ bool gemm_supported(int64_t M, int64_t N, int64_t K, bool gated) {
          M <= ((int64_t)1 << 31) && gemm_tiles(M, N, gated) <= ((int64_t)1 << 23);
 }
 
-// Both kernels take any sizes; the quicker one runs. The few-lines kernel does
-// about 700 TFLOP/s once it is bound by its decode (256 x 8192 x 8192: 48 us);
-// a round of 256 tiles takes 18.3 ns a k and 12 us around them, however few of
-// its 256 lines and of the 256 CUs are in use (512 x 8192 x 8192: 162 us against
-// 97; 1024 x 8192 x 8192: 162 against 196). In units of a product and a sum:
+// Both kernels take any sizes; the quicker one runs, by their times in ns. A
+// few-lines workgroup covers 64 lines of A by 64 of B in 8.5 us and 1.7 ns a k,
+// 256 at a time (512 x 8192 x 8192: 93 us; 4096 x 2816 x 256: 94 us); a round of
+// 256 tiles of 256 x 256 takes 20 us and 18.5 ns a k, however few of its lines
+// and of the CUs are in use (512 x 8192 x 8192: 162 us; 4096 x 2816 x 2816: 77 us).
 static bool few_lines(const GemmArgs& a) {
   const bool gated = a.act == 4;
-  const double lines = (double)((a.M + 63) / 64 * 64), nb = (double)(gated ? 2 * a.N : a.N), K = (double)a.K;
-  // a launch holds fewer than 2^32 threads; the few-lines kernel's tiles are
-  // at least 64 (or all) lines by 16 outputs and have 512
-  if ((lines / 64) * (nb / 16 + 1) > (double)(1 << 22)) return false;
+  const double groups =
+      (double)((a.M + 63) / 64) * (double)(((gated ? 2 * a.N : a.N) + 63) / 64), K = (double)a.K;
+  // a launch holds fewer than 2^32 threads: of the few-lines kernel's narrowest
+  // tiles, 64 (or all) lines by 16 outputs with 512 threads, 2^22
+  if (4 * groups > (double)(1 << 22)) return false;
   const double rounds = (double)((gemm_tiles(a.M, a.N, gated) + 255) / 256);
-  return lines * nb * K < rounds * (6.4e6 * K + 4.2e9);
+  return (groups > 256 ? groups / 256 : 1.0) * (8500 + 1.7 * K) < rounds * (20000 + 18.5 * K);
 }
 
 int launch_gemm(const GemmArgs& a, hipStream_t s) {

@@ -90,17 +90,21 @@ __device__ __forceinline__ float load_bias(const GemmArgs& p, int64_t j) {
 // .., i + (NL - 1) STEP; nj columns (8 or more: all) and the lines below M
 // are in the matrix. z0: pre-activations (the gate's, if gated), z1: the up
 // lines'; both with their bias.
+// res: the residual, from load_residual.
+template <typename T, int NL, int STEP>
+__device__ __forceinline__ void load_residual(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
+                                              Raw8<T> (&res)[NL]) {
+  if (!p.residual || nj <= 0) return;
+#pragma unroll
+  for (int v = 0; v < NL; ++v)
+    if (i + v * STEP < p.M)
+      load8_raw(static_cast<const T*>(p.residual) + (i + v * STEP) * p.N + j, nj, res[v]);
+}
 template <typename T, bool GATED, int NL, int STEP>
 __device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64_t j, int64_t nj,
-                                             float (&z0)[NL][8], float (&z1)[NL][8]) {
+                                             float (&z0)[NL][8], float (&z1)[NL][8],
+                                             const Raw8<T> (&res)[NL]) {
   if (nj <= 0) return;
-  Raw8<T> res[NL];
-  if (p.residual) {
-#pragma unroll
-    for (int v = 0; v < NL; ++v)
-      if (i + v * STEP < p.M)
-        load8_raw(static_cast<const T*>(p.residual) + (i + v * STEP) * p.N + j, nj, res[v]);
-  }
   if (p.z) {
 #pragma unroll
     for (int v = 0; v < NL; ++v)

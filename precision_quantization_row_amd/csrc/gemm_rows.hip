@@ -236,8 +236,14 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p, un
       if constexpr (GATED)
         z1[0][x] = apply_scale(z1[0][x], xs, line_scale(p.b, p.N + jj)) + load_bias(p, p.N + jj);
     }
-    if (p.out_dtype == 0) finish_lines<uint16_t, GATED, 1, 0>(p, i, j, nj, z0, z1);
-    else finish_lines<float, GATED, 1, 0>(p, i, j, nj, z0, z1);
+    auto finish = [&](auto type_) __attribute__((always_inline)) {
+      using T = decltype(type_);
+      Raw8<T> res[1];
+      load_residual<T, 1, 0>(p, i, j, nj, res);
+      finish_lines<T, GATED, 1, 0>(p, i, j, nj, z0, z1, res);
+    };
+    if (p.out_dtype == 0) finish(uint16_t{});
+    else finish(float{});
   }
 }
 

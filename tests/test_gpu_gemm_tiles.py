@@ -4,8 +4,8 @@ definition in 64 bits on the GPU.
 Operands are the exact ones of the small tests (every FP32 sum of their
 products is exact in any order), so z without a bias has to be equal, a bias
 costs one rounding, and y is held to the activation of the z that came back.
-The kernel for few lines takes a product while lines x outputs stay below about
-6.4e6 + 4.2e9 / K (for up to 256 tiles of 256 x 256): every size here is above.
+Which kernel a product takes goes by the times of both; tiles of 256 x 256 take
+those with many lines and outputs, as here.
 """
 import numpy as np
 import pytest
