@@ -101,7 +101,8 @@ int64_t act_bwd_parts(int64_t M, int64_t N) {
 }
 
 template <typename T>
-static int launch_act_bwd_t(const ActBwdArgs& a, hipStream_t s) {
+static int launch_act_bwd_t(ActBwdArgs a, hipStream_t s) {
+  if (act_bwd_parts(a.M, a.N) == 1) a.part = a.dbias;  // one run: its sums are the result
   const int64_t rows = act_bwd_rows(a.M, a.N);
   const dim3 g((unsigned)((a.N + 511) / 512), (unsigned)act_bwd_parts(a.M, a.N)), b(256);
   switch (a.act) {
@@ -112,7 +113,7 @@ static int launch_act_bwd_t(const ActBwdArgs& a, hipStream_t s) {
     default: hipLaunchKernelGGL((act_bwd_kernel<T, ACT_NONE>), g, b, 0, s, a, rows); break;
   }
   if (hipGetLastError() != hipSuccess) return -3;
-  if (!a.dbias) return 0;
+  if (!a.dbias || a.part == a.dbias) return 0;
   return launch_colsum(a.part, act_bwd_parts(a.M, a.N), a.act == ACT_SWIGLU ? 2 * a.N : a.N, a.dbias,
                        a.noop, s);
 }

@@ -456,7 +456,8 @@ static int go_norm_bwd(const NormBwdArgs& a, hipStream_t s) {
 }
 
 template <typename T, typename W>
-static int launch_norm_bwd_t(const NormBwdArgs& a, hipStream_t s) {
+static int launch_norm_bwd_t(NormBwdArgs a, hipStream_t s) {
+  if (norm_bwd_parts(a.M, a.K) == 1) a.part = a.dw;  // one part: it is the result
   const int64_t chunks = (a.K + 7) / 8;
   int rc;
   if (chunks <= 64) rc = go_norm_bwd<T, W, 64, 1>(a, s);
@@ -475,7 +476,7 @@ static int launch_norm_bwd_t(const NormBwdArgs& a, hipStream_t s) {
     rc = hipGetLastError() == hipSuccess ? 0 : -3;
   }
   if (rc) return rc;
-  return a.dw ? launch_colsum(a.part, norm_bwd_parts(a.M, a.K), a.K, a.dw, a.noop, s) : 0;
+  return a.dw && a.part != a.dw ? launch_colsum(a.part, norm_bwd_parts(a.M, a.K), a.K, a.dw, a.noop, s) : 0;
 }
 
 int launch_norm_bwd(const NormBwdArgs& a, hipStream_t s) {
