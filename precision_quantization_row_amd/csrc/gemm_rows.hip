@@ -208,43 +208,55 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p, un
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       *reinterpret_cast<f32x4*>(&part[wave][(16 * m + l16) * PITCH + 16 * n + 4 * g]) = acc[m][n];
-  __syncthreads();
-  // 8 consecutive outputs a thread
+  // 8 consecutive outputs a thread; their factors and biases are loaded while
+  // the waves meet
   constexpr int LPR = 2 * OT;
-#pragma unroll 1
-  for (int e = tid; e < 16 * MT * LPR; e += RW * 64) {
-    const int r = e / LPR, cl = 8 * (e % LPR);
-    const int64_t i = i0 + r, j = j0 + cl, nj = p.N - j;
-    if (i >= p.M || nj <= 0) continue;
-    float z0[1][8] = {}, z1[1][8] = {};
-#pragma unroll 2  // (more sums in flight would cost the main loop its waves)
-    for (int w = 0; w < RW; ++w) {
-      const f32x4* q = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + cl]);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) z0[0][x] += q[x / 4][x % 4];
-      if constexpr (GATED) {
-        const f32x4* qg = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + 16 * OT + cl]);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) z1[0][x] += qg[x / 4][x % 4];
-      }
-    }
-    const LineScale xs = line_scale(p.a, i);
+  static_assert(16 * MT * LPR <= RW * 64, "one run of outputs a thread");
+  const int r = tid / LPR, cl = 8 * (tid % LPR);
+  const int64_t i = i0 + r, j = j0 + cl, nj = p.N - j;
+  const bool live = r < 16 * MT && i < p.M && nj > 0;
+  LineScale xs, w0[8], w1[8];
+  float b0[8], b1[8];
+  if (live) {
+    xs = line_scale(p.a, i);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const int64_t jj = min(j + x, p.N - 1);
-      z0[0][x] = apply_scale(z0[0][x], xs, line_scale(p.b, jj)) + load_bias(p, jj);
-      if constexpr (GATED)
-        z1[0][x] = apply_scale(z1[0][x], xs, line_scale(p.b, p.N + jj)) + load_bias(p, p.N + jj);
+      w0[x] = line_scale(p.b, jj);
+      b0[x] = load_bias(p, jj);
+      if constexpr (GATED) {
+        w1[x] = line_scale(p.b, p.N + jj);
+        b1[x] = load_bias(p, p.N + jj);
+      }
     }
-    auto finish = [&](auto type_) __attribute__((always_inline)) {
-      using T = decltype(type_);
-      Raw8<T> res[1];
-      load_residual<T, 1, 0>(p, i, j, nj, res);
-      finish_lines<T, GATED, 1, 0>(p, i, j, nj, z0, z1, res);
-    };
-    if (p.out_dtype == 0) finish(uint16_t{});
-    else finish(float{});
   }
+  __syncthreads();
+  if (!live) return;
+  float z0[1][8] = {}, z1[1][8] = {};
+#pragma unroll 4  // (all sums in flight would cost the main loop its waves)
+  for (int w = 0; w < RW; ++w) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + cl]);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) z0[0][x] += q[x / 4][x % 4];
+    if constexpr (GATED) {
+      const f32x4* qg = reinterpret_cast<const f32x4*>(&part[w][r * PITCH + 16 * OT + cl]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) z1[0][x] += qg[x / 4][x % 4];
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    z0[0][x] = apply_scale(z0[0][x], xs, w0[x]) + b0[x];
+    if constexpr (GATED) z1[0][x] = apply_scale(z1[0][x], xs, w1[x]) + b1[x];
+  }
+  auto finish = [&](auto type_) __attribute__((always_inline)) {
+    using T = decltype(type_);
+    Raw8<T> res[1];
+    load_residual<T, 1, 0>(p, i, j, nj, res);
+    finish_lines<T, GATED, 1, 0>(p, i, j, nj, z0, z1, res);
+  };
+  if (p.out_dtype == 0) finish(uint16_t{});
+  else finish(float{});
 }
 
 template <bool A8, bool GATED, int MT, int NT>
