@@ -14,7 +14,10 @@ namespace nvfp4 {
 // load its block scales 2 bytes at a time, which costs the memory pipe as much
 // as the codes' 16 (3.0 against 4.6 TB/s at 1 x 8192 x 28672 without them), so
 // the wave loads the 32 scale bytes of each line of a quad in whole and hands
-// them out through its own piece of LDS.
+// them out through its own piece of LDS. Measured: 1 x 57344 x 8192 (E4M3 A) 53 us,
+// 5.0 TB/s; 16 lines, gated, the same size 74 us, where each workgroup's own
+// read of A costs 10; 1 x 4096 x 4096 5.6 us and 128 x 4096 x 4096 11.3 us, which are
+// latency; 256 x 8192 x 8192 48 us, which is decode (705 TFLOP/s).
 
 // The block scales of 16 T lines for one quad, as one wave loads them: 8 bytes
 // a lane (T = 1) or T / 2 times 16.

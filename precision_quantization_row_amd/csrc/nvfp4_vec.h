@@ -19,7 +19,6 @@ typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
