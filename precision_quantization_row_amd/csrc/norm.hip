@@ -341,13 +341,21 @@ __global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormBwdArgs p) {
   }
 }
 
-// Long rows: dx of one row per turn with the row read twice; dw per column
-// chunk by a second launch of norm_dw_long_kernel.
-template <typename T, typename W>
+// Rows too long for the registers, read twice (the second time from L2). Up to
+// SUMS = 32768 columns a workgroup's part of dw stays in LDS, each column with
+// the lane that owns it; longer rows (SUMS = 0) take dw by a launch of their
+// own (norm_dw_long_kernel), which reads dy and h once more. (Rows of 28672 in
+// registers, four runs a lane: spills, 458 us at 4096 rows in BF16.)
+template <typename T, typename W, int SUMS>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
   constexpr int NT = 1024;
   __shared__ float red[2][NT / 64 + 1];
+  __shared__ __attribute__((aligned(16))) float sums[SUMS ? SUMS : 4];
+  if constexpr (SUMS > 0) {
+    const float zero[8] = {};
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < p.K; c += 8 * NT) store8(sums + c, 8, zero);
+  }
   const int64_t K = p.K, step = 8 * NT;
   const W* w = static_cast<const W*>(p.w);
   int turn = 0;
@@ -380,7 +388,22 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdArgs p
         for (int k = 0; k < 8; ++k) dx[k] += t[k];
       }
       store8(static_cast<T*>(p.dx) + row * K + c, n, dx);
+      if constexpr (SUMS > 0) {
+        float d[8];
+        load8(sums + c, 8, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(dy[k], h[k] * r, d[k]);
+        store8(sums + c, 8, d);
+      }
     }
+  }
+  if constexpr (SUMS > 0) {
+    if (p.dw)
+      for (int64_t c = 8 * (int64_t)threadIdx.x; c < K; c += step) {
+        float d[8];
+        load8(sums + c, 8, d);
+        store8(p.part + (int64_t)blockIdx.x * K + c, K - c, d);
+      }
   }
 }
 // dx may be dy's own buffer (the norm's arguments allow it), so for long rows
@@ -467,14 +490,18 @@ static int launch_norm_bwd_t(NormBwdArgs a, hipStream_t s) {
   else if (chunks <= 512) rc = go_norm_bwd<T, W, 256, 2>(a, s);
   else if (chunks <= 1024) rc = go_norm_bwd<T, W, 512, 2>(a, s);
   else if (chunks <= 2048) rc = go_norm_bwd<T, W, 1024, 2>(a, s);
-  else {
+  else if (a.K <= 32768) {
+    hipLaunchKernelGGL((norm_bwd_long_kernel<T, W, 32768>), dim3((unsigned)norm_bwd_parts(a.M, a.K)),
+                       dim3(1024), 0, s, a);
+    rc = hipGetLastError() == hipSuccess ? 0 : -3;
+  } else {
     const int64_t P = norm_bwd_parts(a.M, a.K);
     if (a.dw) {
       hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3((unsigned)((chunks + 255) / 256), (unsigned)P),
                          dim3(256), 0, s, a);
       if (hipGetLastError() != hipSuccess) return -3;
     }
-    hipLaunchKernelGGL((norm_bwd_long_kernel<T, W>), dim3((unsigned)P), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((norm_bwd_long_kernel<T, W, 0>), dim3((unsigned)P), dim3(1024), 0, s, a);
     rc = hipGetLastError() == hipSuccess ? 0 : -3;
   }
   if (rc) return rc;
