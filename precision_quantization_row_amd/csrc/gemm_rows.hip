@@ -166,20 +166,24 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p, un
       __builtin_amdgcn_sched_barrier(0);  // (decoded ahead, fragments would cost waves)
     }
   };
+  // This wave's units u0 .. u1 - 1: whole quads, or, with PD 2, pairs where k is
+  // too short for quads to reach all waves.
   const int nu = (K + 127) / 128, nq = (nu + 3) / 4, per = (nq + RW - 1) / RW;
-  const int q0 = wave * per, u1 = min(nu, 4 * (q0 + per));
+  const bool pairs = PD < 4 && nu <= 2 * RW;
+  const int q0 = pairs ? wave / 2 : wave * per, u0 = pairs ? 2 * wave : 4 * q0;
+  const int u1 = min(nu, pairs ? u0 + 2 : 4 * (q0 + per));
   static_for<2>([&](auto i) __attribute__((always_inline)) {
     constexpr int h = decltype(i)::value;
-    if (4 * (q0 + h) < u1) {
+    if ((PD >= 4 || u0 < u1) && 4 * (q0 + h) < u1) {
       qsb.template load<h>(sb, su, lane, q0 + h, sp);
       if constexpr (!A8) qsa.template load<h>(sa, sa, lane, q0 + h, sp);
     }
   });
   static_for<PD>([&](auto i) __attribute__((always_inline)) {
-    if (4 * q0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], 4 * q0 + decltype(i)::value);
+    if (u0 + decltype(i)::value < u1) fetch(ring[decltype(i)::value], u0 + decltype(i)::value);
   });
 #pragma unroll 1
-  for (int q2 = q0; 4 * q2 < u1; q2 += 2)
+  for (int q2 = q0; (PD >= 4 || u0 < u1) && 4 * q2 < u1; q2 += 2)
     static_for<2>([&](auto h_) __attribute__((always_inline)) {
       constexpr int h = decltype(h_)::value;
       const int q = q2 + h;
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(RW * 64) gemm_rows_kernel(const GemmArgs p, un
         static_for<4>([&](auto i) __attribute__((always_inline)) {
           constexpr int s = decltype(i)::value, r = (4 * h + s) % PD;
           const int u = 4 * q + s;
-          if (u < u1) {
+          if ((PD >= 4 || u >= u0) && u < u1) {  // (PD 4: u0 begins a quad)
             multiply(ring[r], s);
             if (u + PD < u1) fetch(ring[r], u + PD);
           }
