@@ -456,13 +456,18 @@ def _raw_stream(stream, dev) -> int:
 
 def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream):
     """(tensor, address, bytes) of the workspace: the caller's (any dtype), or
-    one from torch's allocator, which orders its reuse on the stream."""
+    one from torch's allocator. That one comes from the pool of the stream the
+    call runs on: what used the block before, and what takes it after, is in
+    that stream's order. (A block of the current stream's pool could still be
+    in use by work queued there.)"""
     if need <= 0:
         return None, None, 0
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
     if not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     size = ws.numel() * ws.element_size()
