@@ -407,12 +407,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdArgs p
   }
 }
 // dx may be dy's own buffer (the norm's arguments allow it), so for long rows
-// dw is taken before dx is written. Workgroup (bx, by): 2048 columns, rows
-// by, by + gridDim.y, ...
+// dw is taken before dx is written. Workgroup (bx, by): 2048 columns from c0
+// on, rows by, by + gridDim.y, ...
 template <typename T>
-__global__ void __launch_bounds__(256) norm_dw_long_kernel(const NormBwdArgs p) {
+__global__ void __launch_bounds__(256) norm_dw_long_kernel(const NormBwdArgs p, int64_t c0) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
-  const int64_t K = p.K, c = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x), n = K - c;
+  const int64_t K = p.K, c = c0 + 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x), n = K - c;
   if (n <= 0) return;
   float dw[8] = {};
   for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y) {
@@ -429,13 +429,13 @@ __global__ void __launch_bounds__(256) norm_dw_long_kernel(const NormBwdArgs p) 
 // out[c] = sum over i of part[i][c]: 32 strands of rows, each in order, then the
 // strands in order. A workgroup owns 32 columns; a strand keeps 8 loads on
 // their way (64 columns, 16 strands and one load: 25 us of norm_bwd's 52 at
-// 4097 x 2881).
+// 4097 x 2881). c0: the launch's first column.
 __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int64_t P, int64_t N,
-                                                      float* out, const float* noop) {
+                                                      float* out, const float* noop, int64_t c0) {
   if (noop != nullptr && *noop == 1.0f) return;
   __shared__ float acc[32][33];
   const int col = threadIdx.x & 31, strand = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  const int64_t c = c0 + (int64_t)blockIdx.x * 32 + col;
   float s = 0.0f;
   if (c < N) {
     const float* q = part + c;
@@ -459,11 +459,23 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int64_t
   }
 }
 
+// Wider inputs take several launches, too: 2^26 columns are 2^31 threads of
+// colsum_kernel (32 a column), and of norm_dw_long_kernel with 256 parts.
+template <typename F>
+static int go_columns(int64_t N, F launch) {
+  for (int64_t c = 0; c < N; c += 1 << 26) {
+    launch(c, std::min<int64_t>(N - c, 1 << 26));
+    if (hipGetLastError() != hipSuccess) return -3;
+  }
+  return 0;
+}
+
 int launch_colsum(const float* part, int64_t P, int64_t N, float* out, const float* noop,
                   hipStream_t s) {
-  hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(1024), 0, s, part, P, N,
-                     out, noop);
-  return hipGetLastError() == hipSuccess ? 0 : -3;
+  return go_columns(N, [=](int64_t c0, int64_t n) {
+    hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((n + 31) / 32)), dim3(1024), 0, s, part, P, N, out,
+                       noop, c0);
+  });
 }
 
 // Workgroups of the backward pass, a function of the sizes alone so that the
@@ -497,9 +509,11 @@ static int launch_norm_bwd_t(NormBwdArgs a, hipStream_t s) {
   } else {
     const int64_t P = norm_bwd_parts(a.M, a.K);
     if (a.dw) {
-      hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3((unsigned)((chunks + 255) / 256), (unsigned)P),
-                         dim3(256), 0, s, a);
-      if (hipGetLastError() != hipSuccess) return -3;
+      rc = go_columns(a.K, [&](int64_t c0, int64_t n) {
+        hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3((unsigned)((n + 2047) / 2048), (unsigned)P),
+                           dim3(256), 0, s, a, c0);
+      });
+      if (rc) return rc;
     }
     hipLaunchKernelGGL((norm_bwd_long_kernel<T, W, 0>), dim3((unsigned)P), dim3(1024), 0, s, a);
     rc = hipGetLastError() == hipSuccess ? 0 : -3;
