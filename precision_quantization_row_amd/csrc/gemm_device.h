@@ -13,9 +13,9 @@
 // Arithmetic. e2m1 has 2 significant bits and e4m3 has 4: u and v have at
 // most 6 and lie in [2^-10, 2688], so binary16 holds them exactly and the
 // matrix instructions take them as they are; products and sums are FP32. The
-// second-level factors are applied once per output: their mantissas are
-// multiplied and their exponents added, so that neither a huge times a tiny
-// amax nor an intermediate product leaves the FP32 range on the way.
+// second-level factors (amaxes and f) are applied once per output: their
+// mantissas are multiplied and their exponents added, so that neither a huge
+// times a tiny one nor an intermediate product leaves the FP32 range on the way.
 #pragma once
 
 #include "nvfp4_launch.h"
@@ -71,12 +71,12 @@ __device__ __forceinline__ h8 decode8_fp8(uint32_t w0, uint32_t w1) {
 
 // ---------------------------------------------------------------- epilogue
 struct LineScale {
-  float m;  // mantissa of the amax times f_inv
-  int e;    // its exponent
+  float m;  // mantissas of the amax and of f, multiplied: [1/4, 1)
+  int e;    // exponents, added
 };
 __device__ __forceinline__ LineScale line_scale(const GemmOperand& o, int64_t line) {
   const float a = o.amax[o.mode == 0 ? 0 : line];
-  return {__builtin_amdgcn_frexp_mantf(a) * o.f_inv, __builtin_amdgcn_frexp_expf(a)};
+  return {__builtin_amdgcn_frexp_mantf(a) * o.f_m, __builtin_amdgcn_frexp_expf(a) + o.f_e};
 }
 __device__ __forceinline__ float apply_scale(float acc, const LineScale& x, const LineScale& w) {
   return __builtin_amdgcn_ldexpf(acc * (x.m * w.m), x.e + w.e);

@@ -315,6 +315,15 @@ static bool valid_dtype(int d) { return d == NVFP4_BF16 || d == NVFP4_FP32; }
 constexpr int64_t kMaxSize = (int64_t)1 << 40;   // beyond: an argument error
 constexpr int64_t kMaxCols = (int64_t)1 << 27;   // of the row-wise kernels
 
+// 1 / f as the product's kernels take it: rounded to FP32 as the FP32 quotient is
+// (a quotient of 24-bit numbers may be rounded to 53 bits first), but in parts,
+// since that of a bound below 2^-131 is larger than any FP32 number.
+static void set_factor(GemmOperand* o, float f) {
+  int e;
+  o->f_m = (float)frexp(1.0 / (double)f, &e);
+  o->f_e = e;
+}
+
 int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, const float* a_amax,
                float a_bound, const uint8_t* b, const uint8_t* b_scale, int b_mode,
                const float* b_amax, float b_bound, int64_t M, int64_t N, int64_t K,
@@ -333,9 +342,10 @@ int nvfp4_gemm(int a_fmt, const uint8_t* a, const uint8_t* a_scale, int a_mode, 
   if (!valid_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype))) return NVFP4_ERR_ARG;
   if (!gemm_supported(M, N, K, act == NVFP4_ACT_SWIGLU)) return NVFP4_ERR_UNSUPPORTED;
   GemmArgs g;
-  g.a = {a, a_scale, a_amax, a_mode,
-         a_fmt == NVFP4_FMT_E4M3 ? 1.0f / 448.0f : 1.0f / (a_bound * 6.0f)};
-  g.b = {b, b_scale, b_amax, b_mode, 1.0f / (b_bound * 6.0f)};
+  g.a = {a, a_scale, a_amax, a_mode};
+  set_factor(&g.a, a_fmt == NVFP4_FMT_E4M3 ? 448.0f : a_bound * 6.0f);
+  g.b = {b, b_scale, b_amax, b_mode};
+  set_factor(&g.b, b_bound * 6.0f);
   g.M = M;
   g.N = N;
   g.K = K;

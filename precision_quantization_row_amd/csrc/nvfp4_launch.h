@@ -133,7 +133,8 @@ struct GemmOperand {
   const uint8_t* s;   // block scales, NULL for E4M3 lines
   const float* amax;
   int mode;           // 0 one amax, 1 one per line
-  float f_inv;        // 1 / (bound * 6), 1 / 448 for E4M3 lines
+  float f_m;          // 1 / (bound * 6), or 1 / 448 for E4M3 lines: f_m 2^f_e,
+  int f_e;            // f_m in [1/2, 1]
 };
 struct GemmArgs {
   GemmOperand a, b;
