@@ -1,86 +1,11 @@
-"""The widest and tallest sizes. Every launch of the product, norm and gradient calls at the largest sizes they
-accept: fewer than 2^32 threads, at most 65535 workgroups along y. The library
-runs in a process of its own on stand-ins for the runtime's launch calls, which
-note grids and launch nothing (addresses are never used)."""
-import ctypes
-import json
-import os
-import subprocess
-import sys
-
+"""The widest and tallest sizes. Every launch of the product, norm and gradient
+calls at the largest sizes they accept: fewer than 2^32 threads, at most 65535
+workgroups along y."""
 import pytest
 
+import launch_stub
 import precision_quantization_row_amd as p
-
-STUB = r"""
-#include <stddef.h>
-#include <stdint.h>
-typedef struct { uint32_t x, y, z; } dim3;
-static dim3 grid_, block_;
-static size_t shared_;
-static void* stream_;
-static uint32_t notes[4096][6];
-static int count;
-int __hipPushCallConfiguration(dim3 g, dim3 b, size_t s, void* st) {
-  grid_ = g; block_ = b; shared_ = s; stream_ = st;
-  return 0;
-}
-int __hipPopCallConfiguration(dim3* g, dim3* b, size_t* s, void** st) {
-  *g = grid_; *b = block_; *s = shared_; *st = stream_;
-  return 0;
-}
-int hipLaunchKernel(const void* f, dim3 g, dim3 b, void** args, size_t s, void* st) {
-  if (count < 4096) {
-    uint32_t* n = notes[count++];
-    n[0] = g.x; n[1] = g.y; n[2] = g.z; n[3] = b.x; n[4] = b.y; n[5] = b.z;
-  }
-  return 0;
-}
-int hipGetLastError(void) { return 0; }
-int taken(uint32_t* out) {
-  const int n = count;
-  for (int i = 0; i < n * 6; ++i) out[i] = notes[i / 6][i % 6];
-  count = 0;
-  return n;
-}
-"""
-
-RUN = r"""
-import ctypes, json, sys
-stub = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)   # found before the runtime's own
-lib = ctypes.CDLL(sys.argv[2])
-conv = {"i": ctypes.c_int, "l": ctypes.c_int64, "f": ctypes.c_float, "p": ctypes.c_void_p}
-buf = (ctypes.c_uint32 * (6 * 4096))()
-out = []
-for fn, kinds, args in json.load(sys.stdin):
-    f = getattr(lib, fn)
-    f.restype = ctypes.c_int
-    rc = f(*[conv[k](a) for k, a in zip(kinds, args)])
-    n = stub.taken(buf)
-    out.append([rc, [list(buf[6 * i:6 * i + 6]) for i in range(n)]])
-print(json.dumps(out))
-"""
-
-F, W, L = 0x1000, 0x2000, 1 << 40   # (W: the workspace, which is no output)
-
-
-def gemm(M, N, K, act=0, fmt=2):
-    return ["nvfp4_gemm", "ippipfppipflllpiipppipp",
-            [fmt, F, F if fmt == 2 else None, 1, F, 448.0, F, F, 1, F, 448.0, M, N, K, None, 0, act, None, None, F, 0, None, None]]
-
-
-def act(M, N, a=1):
-    return ["nvfp4_act_backward", "ppillippplpp", [F, F, 0, M, N, a, F, F, W, L, None, None]]
-
-
-def norm(M, K, dt=0):
-    return ["nvfp4_rmsnorm", "ppipifllppipipppfpp",
-            [F, None, dt, F, 0, 1e-5, M, K, None, F, 0, None, 0, None, None, None, 448.0, None, None]]
-
-
-def norm_bwd(M, K, dt=0):
-    return ["nvfp4_rmsnorm_backward", "ppipippllppplpp", [F, F, dt, F, 0, F, None, M, K, F, F, W, L, None, None]]
-
+from launch_stub import act, gemm, norm, norm_bwd
 
 COLS = 1 << 27
 SIZES = [(1, COLS), (2, COLS), (2, COLS - 31), (2, COLS - 32), (255, COLS), (256, COLS), (300, COLS), (256, COLS - 2048),
@@ -94,23 +19,14 @@ CALLS += [gemm(*s, act=a, fmt=f) for f in (1, 2) for a in (0, 4)
 
 @pytest.fixture(scope="module")
 def launches(tmp_path_factory):
-    d = tmp_path_factory.mktemp("stub")
-    src, lib = d / "stub.c", d / "libstub.so"
-    src.write_text(STUB)
-    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
-    p.load_library()
-    so = os.path.join(os.path.dirname(p.__file__), "libnvfp4.so")
-    r = subprocess.run([sys.executable, "-c", RUN, str(lib), so], input=json.dumps(CALLS), capture_output=True, text=True,
-                       timeout=100)
-    assert r.returncode == 0, r.stderr
-    return json.loads(r.stdout)
+    return launch_stub.launches(CALLS, tmp_path_factory.mktemp("stub"))[1]
 
 
 @pytest.mark.parametrize("i", range(len(CALLS)), ids=lambda i: f"{i}-{CALLS[i][0]}")
 def test_threads_of_a_launch(launches, i):
     rc, grids = launches[i]
     assert rc == p.NVFP4_OK and grids, CALLS[i]
-    for gx, gy, gz, bx, by, bz in grids:
+    for _, gx, gy, gz, bx, by, bz in grids:
         assert gz == by == bz == 1 and 1 <= bx <= 1024
         assert gx >= 1 and 1 <= gy <= 65535
         assert gx * gy * bx < 1 << 32, (CALLS[i], gx, gy, bx)
@@ -118,9 +34,8 @@ def test_threads_of_a_launch(launches, i):
 
 def test_the_stand_ins_see_the_launch(launches):
     """One row: one launch of one workgroup a row, so the grids above are real ones."""
-    assert ctypes.sizeof(ctypes.c_uint32) == 4
     k = CALLS.index(norm(1, COLS))
-    assert launches[k][1] == [[1, 1, 1, 1024, 1, 1]]
+    assert [g[1:] for g in launches[k][1]] == [[1, 1, 1, 1024, 1, 1]]
 
 
 @pytest.mark.gpu
