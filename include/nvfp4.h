@@ -349,7 +349,9 @@ int64_t nvfp4_act_backward_workspace(int64_t M, int64_t N, int act);
  *   y [M][K] of y_dtype or NULL; rstd [M] float or NULL: r, for the backward
  *   row_amax [M] float, required with q; q_fmt NONE: q and s NULL
  *   bound: NVFP4 only (0 < bound <= 448)
- * At least one output. sum_k h_k^2 has to stay below FLT_MAX. K above 2^27 is
+ * At least one output. sum_k h_k^2 has to stay below FLT_MAX. A row of h that
+ * holds a NaN or an infinity gets a NaN row_amax, which makes whatever is decoded from
+ * its codes NaN; other rows are not affected. K above 2^27 is
  * NVFP4_ERR_UNSUPPORTED. */
 int nvfp4_rmsnorm(const void* x, const void* residual, int in_dtype, const void* weight,
                   int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y, int y_dtype,

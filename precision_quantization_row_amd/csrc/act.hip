@@ -7,7 +7,8 @@
 // 512 columns (8 a lane) and a run of rows, every fourth of them a wave; the
 // bias gradient's sums stay in registers, meet in LDS, go to one workspace row
 // per run, and are added in order by a second kernel (no atomics). 8192 x
-// (2 x 28672) BF16, gated: 446 us, 5.3 TB/s; 4097 x 2881 FP32 with a bias: 26 + 4 us.
+// (2 x 28672) BF16, gated: 446 us, 5.3 TB/s; 4097 x 2881 FP32 with a bias: 34 + 4 us
+// from HBM, 25 + 4 where the 142 MB are still in the memory-side cache.
 #include "nvfp4_launch.h"
 #include "nvfp4_vec.h"
 

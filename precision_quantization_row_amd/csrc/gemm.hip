@@ -9,11 +9,16 @@ bool gemm_supported(int64_t M, int64_t N, int64_t K, bool gated) {
          M <= ((int64_t)1 << 31) && gemm_tiles(M, N, gated) <= ((int64_t)1 << 23);
 }
 
-// Both kernels take any sizes; the quicker one runs, by their times in ns. A
-// few-lines workgroup covers 64 lines of A by 64 of B in 8.5 us and 1.7 ns a k,
-// 256 at a time (512 x 8192 x 8192: 93 us; 4096 x 2816 x 256: 94 us); a round of
-// 256 tiles of 256 x 256 takes 20 us and 18.5 ns a k, however few of its lines
-// and of the CUs are in use (512 x 8192 x 8192: 162 us; 4096 x 2816 x 2816: 77 us).
+// Both kernels take any sizes; the quicker one runs, by a model of their times
+// in ns. A few-lines workgroup is counted as 64 lines of A by 64 of B in 8.5 us
+// and 1.7 ns a k, 256 at a time (512 x 8192 x 8192: 90 us, measured 93-100; 4096 x
+// 2816 x 256: 98 us, 91); a round of 256 tiles of 256 x 256 takes 20 us and 18.5 ns
+// a k, however few of its lines and of the CUs are in use (512 x 8192 x 8192: 172
+// us, measured 155-162; 4096 x 2816 x 2816: 72 us, 70-77). The model is coarse: 32
+// lines and fewer take narrower tiles and half the time it says, odd k nearly
+// twice. Where the two are near each other it decides well: of 26 sizes from 16 x
+// 4096 x 4096 to 8192 x 4096 x 256 none took over 1.07 times the quicker kernel (2048
+// x 2048 x 1024, the nearest: 32.5 against 33.7 us).
 static bool few_lines(const GemmArgs& a) {
   const bool gated = a.act == 4;
   const double groups =

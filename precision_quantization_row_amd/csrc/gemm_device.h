@@ -137,7 +137,7 @@ __device__ __forceinline__ void finish_lines(const GemmArgs& p, int64_t i, int64
     if (i + v * STEP < p.M) store8(static_cast<T*>(p.y) + (i + v * STEP) * p.N + j, nj, z0[v]);
 }
 
-// 16 bytes of a packed line from byte `off` on; bytes past the line's end read
+// 4 bytes of a packed line from byte `off` on; bytes past the line's end read
 // as zero. Only bytes of the line are touched: a dword that would cross the
 // end is read from the line's last 4 bytes and shifted down (lines of 4 bytes
 // and more; shorter ones byte by byte).

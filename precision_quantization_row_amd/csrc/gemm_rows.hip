@@ -14,10 +14,11 @@ namespace nvfp4 {
 // load its block scales 2 bytes at a time, which costs the memory pipe as much
 // as the codes' 16 (3.0 against 4.6 TB/s at 1 x 8192 x 28672 without them), so
 // the wave loads the 32 scale bytes of each line of a quad in whole and hands
-// them out through its own piece of LDS. Measured: 1 x 57344 x 8192 (E4M3 A) 53 us,
-// 5.0 TB/s; 16 lines, gated, the same size 74 us, where each workgroup's own
-// read of A costs 10; 1 x 4096 x 4096 5.6 us and 128 x 4096 x 4096 11.3 us, which are
-// latency; 256 x 8192 x 8192 48 us, which is decode (705 TFLOP/s).
+// them out through its own piece of LDS. Measured: 1 x 57344 x 8192 (E4M3 A) 53-56
+// us, 4.7-5.0 TB/s; 16 lines, gated, the same size 74 us, where each workgroup's
+// own read of A costs 10; 1 x 4096 x 4096 5.6 us, which is latency; 128 x 4096 x 4096
+// 11.3 us, two latencies one after the other, as a wave has 4 units of k and 2 on
+// their way; 256 x 8192 x 8192 49 us, which is decode (702 TFLOP/s).
 
 // The block scales of 16 T lines for one quad, as one wave loads them: 8 bytes
 // a lane (T = 1) or T / 2 times 16.
@@ -274,10 +275,11 @@ static void go_rows(const GemmArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((gemm_rows_kernel<A8, GATED, MT, NT>), dim3(gm * gn), dim3(RW * 64), 0, s, a, gn);
 }
 
-// The tile of a few-lines launch: the widest one that leaves a workgroup for
-// each of the 256 CUs. (1 x 57344 x 8192: NT 2 with 4 units on their way 54 us,
-// NT 4 with 2 64 us, NT 4 with 4 73 us: the registers cost it the second
-// workgroup of a CU.)
+// The tile of a few-lines launch. Up to 16 lines of A: 32 lines of B, or 16 if
+// that leaves CUs without a workgroup (1 x 57344 x 8192: 32 lines with 4 units on
+// their way 54 us, 64 with 2 64 us, 64 with 4 73 us: the registers cost it the
+// second workgroup of a CU). Up to 32: 32 by 32. More: 64 by 64, or by 32 if 64
+// leaves CUs without a workgroup.
 template <bool A8, bool GATED>
 static void launch_rows_t(const GemmArgs& a, hipStream_t s) {
   const int64_t mt = (a.M + 15) / 16;

@@ -20,10 +20,10 @@ namespace nvfp4 {
 // 560 of a stage's 2048 cycles there; this shape spends 430 + 560.
 //
 // Bound by the matrix pipe and, with real data, by power: 8192 x 8192 x 28672
-// takes 2790-2860 us (1.35-1.38 PFLOP/s; a library product of dense bf16
-// matrices 2617), and 2111 on zeros; 8192^3 874 us, the pipe busy 73 % of the
-// cycles. Around its products a round of tiles spends 20 us (4096 x 2816 x 256:
-// 24 us, 13 of them the stores of 46 MB).
+// takes 2790-2970 us, by card and codes (1.30-1.38 PFLOP/s; a library product of
+// dense bf16 matrices 2617), and 2111 on zeros; 8192^3 842-874 us, the pipe busy
+// 73 % of the cycles. Around its products a round of tiles spends 20 us (4096 x
+// 2816 x 256: 21-24 us, 13 of them the stores of 46 MB).
 //
 // k order. Stage u is the chunks 2 u and 2 u + 1 of 32 k; slice d of it takes
 // codes 8 d .. 8 d + 7 of both, the two halves of the wave one chunk each. Both

@@ -17,7 +17,8 @@
 // Both are bound by HBM: a row is read once into registers, reduced there and
 // written once. 16384 x 4096 BF16 with the residual: forward 71 us (6.6 TB/s, partly
 // from the memory-side cache), backward 95 us and 4.5 for its column sums
-// (5.3 TB/s); 4097 x 2881 FP32 backward 27 + 5 us; one row of 8192 forward 3.9 us.
+// (5.3 TB/s); 4097 x 2881 FP32 backward 35 + 5 us from HBM (27 + 5 from the
+// memory-side cache); one row of 8192 forward 3.9 us.
 #include "nvfp4_launch.h"
 #include "nvfp4_vec.h"
 
@@ -52,7 +53,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
-// Writes one lane's 8 values of a row as codes. c: first column (a multiple
+// Writes one lane's 8 values of a row as codes. NaN clamps to 448 in 8 bits: the
+// row's amax, NaN as well, is what carries it. c: first column (a multiple
 // of 8), n: elements of the row from c on. The lane pair (2i, 2i + 1) holds
 // one 16-element block; both lanes are active (lanes past the row hold zeros).
 __device__ __forceinline__ void write_codes(const NormArgs& p, int64_t row, int64_t c, int64_t n,
@@ -344,8 +346,8 @@ __global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormBwdArgs p) {
 // Rows too long for the registers, read twice (the second time from L2). Up to
 // SUMS = 32768 columns a workgroup's part of dw stays in LDS, each column with
 // the lane that owns it; longer rows (SUMS = 0) take dw by a launch of their
-// own (norm_dw_long_kernel), which reads dy and h once more. (Rows of 28672 in
-// registers, four runs a lane: spills, 458 us at 4096 rows in BF16.)
+// own (norm_dw_long_kernel), which reads dy and h once more. (4096 x
+// 28672 BF16 with dres 225 us; in registers, four runs a lane: spills, 458.)
 template <typename T, typename W, int SUMS>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
@@ -479,7 +481,11 @@ int launch_colsum(const float* part, int64_t P, int64_t N, float* out, const flo
 }
 
 // Workgroups of the backward pass, a function of the sizes alone so that the
-// workspace and the order of the sums do not depend on the device.
+// workspace and the order of the sums do not depend on the device: as many as
+// the BF16 kernels keep resident (126 registers: 4 waves a SIMD). The FP32 ones
+// hold 134 and 138, one workgroup a CU fewer, and up to 16384 columns 128 with 9
+// spilled; from HBM that does not show (4096 x 8192 82 us, 4096 x 16384 163 us, 4.9
+// TB/s, as in BF16).
 int64_t norm_bwd_parts(int64_t M, int64_t K) {
   const int64_t per_cu = K <= 4096 ? 4 : (K <= 8192 ? 2 : 1);
   return std::min<int64_t>(M, 256 * per_cu);

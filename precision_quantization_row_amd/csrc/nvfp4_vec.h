@@ -123,7 +123,8 @@ constexpr float kGeluB = 0.044715f;
 enum { ACT_NONE = 0, ACT_GELU = 1, ACT_SILU = 2, ACT_RELU2 = 3, ACT_SWIGLU = 4 };
 
 // 1 / (1 + e^-x): e^-x = +inf gives 0, as it should; NaN stays NaN. The
-// reciprocal is the hardware's (1 ulp).
+// reciprocal is the hardware's (1 ulp); it flushes results below 2^-126, so for
+// x < -87.3 silu and its slope are 0 where they should be up to 1e-36.
 __device__ __forceinline__ float sigmoid_f(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
