@@ -83,7 +83,10 @@ typedef enum {
   NVFP4_FMT_NONE = 0,
   NVFP4_FMT_E4M3 = 1, /* one E4M3 byte an element, one amax a line (or one for
                          the tensor), no block scales: value = byte * a / 448  */
-  NVFP4_FMT_NVFP4 = 2 /* packed codes, block scales and amax, as above          */
+  NVFP4_FMT_NVFP4 = 2, /* packed codes, block scales and amax, as above         */
+  NVFP4_FMT_INT8 = 3  /* one signed byte an element in [-127, 127], one amax a
+                         line: value = byte * a / 127. The layer norm and the
+                         cache take it; nvfp4_gemm and nvfp4_rmsnorm do not     */
 } nvfp4_format;
 
 /* Activation of the product's epilogue. */
@@ -373,6 +376,143 @@ int nvfp4_rmsnorm_backward(const void* dy, const void* h, int in_dtype, const vo
                            void* dx, float* dweight, void* workspace, int64_t workspace_bytes,
                            const float* noop, void* stream);
 int64_t nvfp4_rmsnorm_backward_workspace(int64_t M, int64_t K);
+
+/* Lines of 8-bit integers: the operands of nvfp4_int8_gemm.
+ *   row_amax[i] = max_k |x_ik|
+ *   q_ik = the integer nearest to RN(x_ik S), halves to the even one, clamped to
+ *          [-127, 127];  S = amax == 0 ? 1 : min(RN(127 / amax), FLT_MAX)
+ * One pass: the amax is found and the codes are written by one read of the row.
+ *   x [M][K] BF16 or FP32; row_amax [M] float, q [M][K]: both written
+ * A row that holds a NaN gets a NaN amax, which makes every product of its codes
+ * NaN; one that holds an infinity an infinite one (products infinite or NaN);
+ * other rows are not affected. K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_int8_quantize(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax, int8_t* q,
+                        const float* noop, void* stream);
+
+/* Both copies of X as lines of 8-bit integers, each direction with its own amax:
+ * rowwise for the forward product, columnwise (transposed) for the gradients'.
+ * Enqueues nvfp4_amax_rowcol(x, ..., row_amax, col_amax, NULL, noop, 0, stream)
+ * and one pass that writes both copies.
+ *   row_amax [M], col_amax [K], q_row [M][K], q_col [K][M]: all written
+ * M or K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_int8_quantize_rowcol(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax,
+                               float* col_amax, int8_t* q_row, int8_t* q_col, const float* noop,
+                               void* stream);
+
+/* Product of two operands of 8-bit integer lines, one amax for each token (line
+ * of A) and channel (line of B), with nvfp4_gemm's epilogue:
+ *   z_ij = (a_i / 127) (b_j / 127) sum_k u_ik v_jk + bias_j
+ *   y_ij = act(z_ij) + residual_ij
+ * The sums are exact (32-bit integers); a sum, the amax factors, the bias, the
+ * activation and the residual follow in FP32 and each output is rounded once.
+ * Both operands lie line by line along k, so the three products of training are
+ * of this form, from the two copies of nvfp4_int8_quantize_rowcol:
+ *   forward          Y  = X W^T    A = rowwise X,      B = rowwise W
+ *   data gradient    dX = dY W     A = rowwise dY,     B = columnwise W
+ *   weight gradient  dW = dY^T X   A = columnwise dY,  B = columnwise X
+ *   a [M][K], a_mode / a_amax: TENSOR ([1]) or LINE ([M]); ROWGROUP is
+ *     NVFP4_ERR_UNSUPPORTED
+ *   b [N][K] ([2 N][K] for ACT_SWIGLU: N gate lines, then the N up lines of the
+ *     same outputs), b_mode / b_amax: TENSOR ([1]) or LINE ([N] or [2 N])
+ *   bias, act, residual, z, y: as nvfp4_gemm
+ * Bytes of -128 count as they are. M, N, K >= 1, any values and any alignment of
+ * the operands. K of 2^17 and more could leave 32 bits and is
+ * NVFP4_ERR_UNSUPPORTED (a longer sum is several calls, y its own residual), as
+ * are N above 2^26 and products of more than 2^23 tiles of 256 x 256. No
+ * workspace is needed. */
+int nvfp4_int8_gemm(const int8_t* a, int a_mode, const float* a_amax, const int8_t* b, int b_mode,
+                    const float* b_amax, int64_t M, int64_t N, int64_t K, const void* bias,
+                    int bias_dtype, int act, const void* residual, void* z, void* y, int out_dtype,
+                    const float* noop, void* stream);
+
+/* Layer norm with the residual's addition, quantized on the way out, one read of
+ * the row:
+ *   h_k = x_k + residual_k (FP32);  mu = sum_k h_k / K
+ *   r = 1 / sqrt(sum_k (h_k - mu)^2 / K + eps)
+ *   y_k = (h_k - mu) r w_k + b_k;  row_amax = max_k |y_k|
+ *   q_fmt E4M3 or NVFP4: as nvfp4_rmsnorm, an A operand of nvfp4_gemm
+ *   q_fmt INT8: q [M][K], the codes of nvfp4_int8_quantize of the FP32 y, an A
+ *               operand of nvfp4_int8_gemm
+ *   x, residual (or NULL) [M][K] of in_dtype; weight, bias (or NULL) [K] of
+ *   w_dtype; eps >= 0
+ *   h [M][K] of in_dtype or NULL: the sum, rounded (may be x or residual)
+ *   y [M][K] of y_dtype or NULL; mean, rstd [M] float or NULL: mu and r, for the
+ *   backward pass
+ *   row_amax [M] float, required with q; q_fmt NONE: q and s NULL
+ *   bound: NVFP4 only (0 < bound <= 448)
+ * At least one output. sum_k |h_k| and sum_k (h_k - mu)^2 have to stay below
+ * FLT_MAX. A row of h that holds a NaN or an infinity gets a NaN mean, rstd and
+ * row_amax; other rows are not affected. K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_layernorm(const void* x, const void* residual, int in_dtype, const void* weight,
+                    const void* bias, int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y,
+                    int y_dtype, float* mean, float* rstd, int q_fmt, uint8_t* q, uint8_t* s,
+                    float* row_amax, float bound, const float* noop, void* stream);
+
+/* Backward pass of nvfp4_layernorm: with xh_k = (h_k - mu) r and g_k = dy_k w_k
+ *   dx_k = r (g_k - sum_j(g_j) / K - xh_k sum_j(g_j xh_j) / K) + dres_k
+ *   dweight_k = sum over rows of dy_k xh_k,  dbias_k = sum over rows of dy_k
+ *               (in an order that depends on the sizes alone)
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h, dres (or NULL: the gradient that reaches h by other ways), dx
+ *   [M][K] of in_dtype, dx may be dy or dres; weight [K] of w_dtype;
+ *   mean, rstd [M] from the forward pass; dweight, dbias [K] float or NULL
+ *   workspace: nvfp4_layernorm_backward_workspace bytes, needed with dweight or
+ *   dbias only.
+ * K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+int nvfp4_layernorm_backward(const void* dy, const void* h, int in_dtype, const void* weight,
+                             int w_dtype, const float* mean, const float* rstd, const void* dres,
+                             int64_t M, int64_t K, void* dx, float* dweight, float* dbias,
+                             void* workspace, int64_t workspace_bytes, const float* noop,
+                             void* stream);
+int64_t nvfp4_layernorm_backward_workspace(int64_t M, int64_t K);
+
+/* A cache of keys and values in pages, quantized as it is written. A line is what
+ * one head of one token holds: D elements with an amax of their own.
+ *   q    [pages][page_size][H][D] bytes (fmt E4M3, INT8), or
+ *        [pages][page_size][H][ceil(D/2)] codes (fmt NVFP4)
+ *   s    [pages][page_size][H][ceil(D/16)] block scales (NVFP4, else NULL)
+ *   amax [pages][page_size][H] float
+ * Codes and scales are those of nvfp4_quantize_transpose's rowwise copy (NVFP4,
+ * mode LINE), of nvfp4_rmsnorm (E4M3) and of nvfp4_int8_quantize (INT8), the
+ * lines being rows.
+ * The tokens of a call lie one after another, sequence by sequence: sequence b has
+ * tokens starts[b] .. starts[b + 1] - 1, at its positions first[b],
+ * first[b] + 1, ... Position n lies at place n mod page_size of page
+ * table[b][n / page_size].
+ *   k, v    [T] rows of H x D elements of in_dtype, k_stride and v_stride
+ *           elements (>= 0) from row to row: slices of a fused projection's
+ *           output as they are. v, v_q, v_s and v_amax NULL: one line a head and
+ *           token (a latent cache)
+ *   table   [B][table_cols] int32 device; starts [B + 1] int32 device, ascending;
+ *           first [B] int32 device, or NULL: zeros
+ * Lengths, positions and the table stay on the device, so the call has a fixed
+ * shape for a captured graph. Rows before starts[0] and from starts[B] on are no
+ * tokens: nothing is written for them. A token whose position is negative, or
+ * past its row of the table, or whose page is not in [0, pages), is skipped;
+ * nothing outside the cache is touched whatever the three arrays hold. Two tokens
+ * of a call must not have the same place (the line would hold bytes of both).
+ * T >= 1, H <= 65535 and D <= 1024, else NVFP4_ERR_UNSUPPORTED (T below 2^31). */
+int nvfp4_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int in_dtype,
+                      int64_t T, int64_t H, int64_t D, int fmt, float bound, int64_t pages,
+                      int64_t page_size, void* k_q, void* k_s, float* k_amax, void* v_q, void* v_s,
+                      float* v_amax, const int32_t* table, int64_t B, int64_t table_cols,
+                      const int32_t* starts, const int32_t* first, const float* noop, void* stream);
+
+/* The cached positions first[b] .. first[b] + starts[b + 1] - starts[b] - 1 of each
+ * sequence as values, in rows starts[b] .. starts[b + 1] - 1 of k and v: the
+ * arguments of nvfp4_cache_write the other way round.
+ *   NVFP4: RN(e2m1(code) RN(RN(e4m3(byte) a) F_inv)), as nvfp4_dequantize;
+ *   E4M3:  RN(byte RN(a / 448));  INT8: RN(byte RN(a / 127));
+ *   out_dtype BF16 rounds that FP32 value once more
+ *   k, v [T] rows, k_stride and v_stride elements (>= H D) apart
+ * Rows of no token are left as they are. A token without a page (as above) reads
+ * as zeros. Limits as nvfp4_cache_write. */
+int nvfp4_cache_read(const void* k_q, const void* k_s, const float* k_amax, const void* v_q,
+                     const void* v_s, const float* v_amax, int fmt, float bound, int64_t pages,
+                     int64_t page_size, const int32_t* table, int64_t B, int64_t table_cols,
+                     const int32_t* starts, const int32_t* first, int64_t T, int64_t H, int64_t D,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride, int out_dtype,
+                     const float* noop, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* nvfp4_status_string(int status);

@@ -40,6 +40,7 @@ NVFP4_FLAG_FORCE_TWO_KERNEL = 1
 NVFP4_FMT_NONE = 0
 NVFP4_FMT_E4M3 = 1
 NVFP4_FMT_NVFP4 = 2
+NVFP4_FMT_INT8 = 3
 
 NVFP4_ACT_NONE = 0
 NVFP4_ACT_GELU = 1
@@ -57,6 +58,9 @@ EXPORTED = ("nvfp4_amax_path", "nvfp4_amax_rowcol", "nvfp4_group_amax_expand",
             "nvfp4_gemm",
             "nvfp4_act_backward", "nvfp4_act_backward_workspace",
             "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace",
+            "nvfp4_int8_quantize", "nvfp4_int8_quantize_rowcol", "nvfp4_int8_gemm",
+            "nvfp4_layernorm", "nvfp4_layernorm_backward", "nvfp4_layernorm_backward_workspace",
+            "nvfp4_cache_write", "nvfp4_cache_read",
             "nvfp4_status_string")
 
 NVFP4_GROUPS_MAX = 256
@@ -126,6 +130,27 @@ def load_library():
                                            i64, f32p, vp]
     lib.nvfp4_rmsnorm_backward_workspace.restype = i64
     lib.nvfp4_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    lib.nvfp4_int8_quantize.restype = c_int
+    lib.nvfp4_int8_quantize.argtypes = [vp, c_int, i64, i64, f32p, vp, f32p, vp]
+    lib.nvfp4_int8_quantize_rowcol.restype = c_int
+    lib.nvfp4_int8_quantize_rowcol.argtypes = [vp, c_int, i64, i64, f32p, f32p, vp, vp, f32p, vp]
+    lib.nvfp4_int8_gemm.restype = c_int
+    lib.nvfp4_int8_gemm.argtypes = [vp, c_int, f32p, vp, c_int, f32p, i64, i64, i64, vp, c_int, c_int, vp,
+                                    vp, vp, c_int, f32p, vp]
+    lib.nvfp4_layernorm.restype = c_int
+    lib.nvfp4_layernorm.argtypes = [vp, vp, c_int, vp, vp, c_int, c_f, i64, i64, vp, vp, c_int, f32p, f32p,
+                                    c_int, u8p, u8p, f32p, c_f, f32p, vp]
+    lib.nvfp4_layernorm_backward.restype = c_int
+    lib.nvfp4_layernorm_backward.argtypes = [vp, vp, c_int, vp, c_int, f32p, f32p, vp, i64, i64, vp, f32p,
+                                             f32p, vp, i64, f32p, vp]
+    lib.nvfp4_layernorm_backward_workspace.restype = i64
+    lib.nvfp4_layernorm_backward_workspace.argtypes = [i64, i64]
+    lib.nvfp4_cache_write.restype = c_int
+    lib.nvfp4_cache_write.argtypes = [vp, i64, vp, i64, c_int, i64, i64, i64, c_int, c_f, i64, i64, vp, vp,
+                                      f32p, vp, vp, f32p, vp, i64, i64, vp, vp, f32p, vp]
+    lib.nvfp4_cache_read.restype = c_int
+    lib.nvfp4_cache_read.argtypes = [vp, vp, f32p, vp, vp, f32p, c_int, c_f, i64, i64, vp, i64, i64, vp, vp,
+                                     i64, i64, i64, vp, i64, vp, i64, c_int, f32p, vp]
     _lib = lib
     return lib
 
@@ -610,6 +635,260 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
         _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_rmsnorm_backward", st)
+
+
+# -------------------------------- 8-bit integers, layer norm, quantized cache
+_I8 = (torch.int8,)
+_I32 = (torch.int32,)
+
+
+def nvfp4_int8_quantize(x: torch.Tensor, row_amax: torch.Tensor, q: torch.Tensor,
+                        noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of x [M, K] as 8-bit integers: row_amax [M] float32 and q [M, K] int8,
+    both written; value = q * row_amax / 127."""
+    lib = _lib or load_library()
+    dev = _first(x, "x", _OUT_CODES)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    st = lib.nvfp4_int8_quantize(_arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
+                                 _arg(row_amax, "row_amax", _F32, M, dev), _arg(q, "q", _I8, M * K, dev),
+                                 _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_int8_quantize", st)
+
+
+def nvfp4_int8_quantize_rowcol(x: torch.Tensor, row_amax: torch.Tensor, col_amax: torch.Tensor,
+                               q_row: torch.Tensor, q_col: torch.Tensor,
+                               noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Both copies of x [M, K] as 8-bit integers: row_amax [M] and q_row [M, K],
+    col_amax [K] and q_col [K, M] (the transpose), all written."""
+    lib = _lib or load_library()
+    dev = _first(x, "x", _OUT_CODES)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    st = lib.nvfp4_int8_quantize_rowcol(
+        _arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
+        _arg(row_amax, "row_amax", _F32, M, dev), _arg(col_amax, "col_amax", _F32, K, dev),
+        _arg(q_row, "q_row", _I8, M * K, dev), _arg(q_col, "q_col", _I8, M * K, dev),
+        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_int8_quantize_rowcol", st)
+
+
+def nvfp4_int8_gemm(a: torch.Tensor, a_mode: int, a_amax: torch.Tensor, b: torch.Tensor, b_mode: int,
+                    b_amax: torch.Tensor, M: int, N: int, K: int, y: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, act: int = NVFP4_ACT_NONE,
+                    residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                    noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y [M, N] = act(A B^T + bias) + residual of 8-bit integer lines a [M, K] and
+    b [N, K] (2 N lines for NVFP4_ACT_SWIGLU: gate lines, then up lines), each
+    line with its amax (or one for all, NVFP4_AMAX_TENSOR). z, y, residual and
+    bias as in nvfp4_gemm."""
+    lib = _lib or load_library()
+    dev = _first(a, "a", _I8)
+    out = _OUT_CODES.get(getattr(y, "dtype", None))
+    if out is None:
+        raise TypeError("y must be a bfloat16 or float32 tensor")
+    NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
+    same = (y.dtype,)
+    st = lib.nvfp4_int8_gemm(
+        _arg(a, "a", _I8, M * K, dev), a_mode,
+        _arg(a_amax, "a_amax", _F32, M if a_mode == NVFP4_AMAX_LINE else 1, dev),
+        _arg(b, "b", _I8, NB * K, dev), b_mode,
+        _arg(b_amax, "b_amax", _F32, NB if b_mode == NVFP4_AMAX_LINE else 1, dev),
+        M, N, K, _arg(bias, "bias", _OUT_CODES, NB, dev),
+        0 if bias is None else _OUT_CODES[bias.dtype], act,
+        _arg(residual, "residual", same, M * N, dev), _arg(z, "z", same, M * NB, dev),
+        _arg(y, "y", same, M * N, dev), out, _arg(noop, "noop", _F32, 1, dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_int8_gemm", st)
+
+
+_NORM_FORMATS = {torch.float8_e4m3fn: NVFP4_FMT_E4M3, torch.int8: NVFP4_FMT_INT8, torch.uint8: NVFP4_FMT_NVFP4}
+
+
+def nvfp4_layernorm(x: torch.Tensor, weight: torch.Tensor, eps: float, bias: Optional[torch.Tensor] = None,
+                    residual: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                    rstd: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                    s: Optional[torch.Tensor] = None, row_amax: Optional[torch.Tensor] = None,
+                    bound: float = 448.0, noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h = x + residual, y = (h - mean) / deviation * weight + bias of x [M, K],
+    with y's row amax and codes: q float8_e4m3fn or int8 [M, K] (8-bit lines), or
+    uint8 [M, ceil(K/2)] with s [M, ceil(K/16)] (NVFP4). bias has weight's dtype.
+    Outputs not given are not written; mean and rstd are what
+    nvfp4_layernorm_backward takes."""
+    lib = _lib or load_library()
+    dev = _first(x, "x", _OUT_CODES)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    same, wtype = (x.dtype,), getattr(weight, "dtype", None)
+    fmt, qn = NVFP4_FMT_NONE, 0
+    if q is not None:
+        fmt = _NORM_FORMATS.get(q.dtype, NVFP4_FMT_NVFP4)
+        qn = M * ((K + 1) // 2) if fmt == NVFP4_FMT_NVFP4 else M * K
+    st = lib.nvfp4_layernorm(
+        _arg(x, "x", same, M * K, dev), _arg(residual, "residual", same, M * K, dev),
+        _OUT_CODES[x.dtype], _arg(weight, "weight", _OUT_CODES, K, dev), _arg(bias, "bias", (wtype,), K, dev),
+        _OUT_CODES.get(wtype, -1), eps, M, K, _arg(h, "h", same, M * K, dev),
+        _arg(y, "y", _OUT_CODES, M * K, dev), 0 if y is None else _OUT_CODES[y.dtype],
+        _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev), fmt,
+        _arg(q, "q", tuple(_NORM_FORMATS), qn, dev),
+        _arg(s, "s", _SCALE_DTYPES, M * ((K + 15) // 16), dev),
+        _arg(row_amax, "row_amax", _F32, M, dev), bound, _arg(noop, "noop", _F32, 1, dev),
+        _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_layernorm", st)
+
+
+def nvfp4_layernorm_backward_workspace(M: int, K: int) -> int:
+    """Workspace bytes of nvfp4_layernorm_backward with dweight or dbias."""
+    return load_library().nvfp4_layernorm_backward_workspace(M, K)
+
+
+def nvfp4_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                             mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                             dweight: Optional[torch.Tensor] = None,
+                             dbias: Optional[torch.Tensor] = None,
+                             dres: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx [M, K], dweight [K] and dbias [K] (float32) of nvfp4_layernorm from
+    dy [M, K] and the saved h, mean and rstd; dres, the gradient that reaches h by
+    other ways, is added to dx."""
+    lib = _lib or load_library()
+    dev = _first(dy, "dy", _OUT_CODES)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D [M, K]")
+    M, K = dy.shape
+    same = (dy.dtype,)
+    sums = dweight is not None or dbias is not None
+    need = lib.nvfp4_layernorm_backward_workspace(M, K) if sums else 0
+    ws, wp, wb = _workspace(workspace, need, dev, stream)
+    st = lib.nvfp4_layernorm_backward(
+        _arg(dy, "dy", same, M * K, dev), _arg(h, "h", same, M * K, dev), _OUT_CODES[dy.dtype],
+        _arg(weight, "weight", _OUT_CODES, K, dev), _OUT_CODES.get(getattr(weight, "dtype", None), -1),
+        _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev),
+        _arg(dres, "dres", same, M * K, dev), M, K, _arg(dx, "dx", same, M * K, dev),
+        _arg(dweight, "dweight", _F32, K, dev), _arg(dbias, "dbias", _F32, K, dev), wp, wb,
+        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_layernorm_backward", st)
+
+
+_CACHE_FORMATS = {torch.float8_e4m3fn: NVFP4_FMT_E4M3, torch.int8: NVFP4_FMT_INT8, torch.uint8: NVFP4_FMT_NVFP4}
+
+
+def _rows(t, name: str, dtypes, shape, dev):
+    """(address, elements from row to row) of [T, H, D] rows that may lie apart."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.data_ptr(), st if T > 1 else H * D
+
+
+def _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev):
+    """Checked cache buffers: (format, pages, page_size, H, the six addresses)."""
+    fmt = _CACHE_FORMATS.get(getattr(k_q, "dtype", None))
+    if fmt is None:
+        raise TypeError("k_q must be a uint8 (NVFP4), float8_e4m3fn or int8 tensor")
+    if not isinstance(k_amax, torch.Tensor) or k_amax.dim() != 3:
+        raise ValueError("k_amax must be 3-D [pages, page_size, H]")
+    pages, size, H = k_amax.shape
+    lines = pages * size * H
+    width, blocks = ((D + 1) // 2, (D + 15) // 16) if fmt == NVFP4_FMT_NVFP4 else (D, 0)
+    addr = []
+    for n, q, s, a in (("k", k_q, k_s, k_amax), ("v", v_q, v_s, v_amax)):
+        if q is None and (s is not None or a is not None or n == "k"):
+            raise ValueError(f"{n}_q is required")
+        if q is not None and a is None:
+            raise ValueError(f"{n}_amax is required")
+        if q is not None and (s is not None) != (fmt == NVFP4_FMT_NVFP4):
+            raise ValueError(f"{n}_s is for NVFP4 lines, and they need it")
+        addr += [_arg(q, n + "_q", (k_q.dtype,), lines * width, dev),
+                 _arg(s, n + "_s", _SCALE_DTYPES, lines * blocks, dev), _arg(a, n + "_amax", _F32, lines, dev)]
+    return fmt, pages, size, H, addr
+
+
+def _sequences(table, starts, first, dev):
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be 2-D [B, columns]")
+    B, cols = table.shape
+    return (_arg(table, "table", _I32, B * cols, dev), B, cols, _arg(starts, "starts", _I32, B + 1, dev),
+            _arg(first, "first", _I32, B, dev))
+
+
+def nvfp4_cache_write(k: torch.Tensor, v: Optional[torch.Tensor], k_q: torch.Tensor,
+                      k_s: Optional[torch.Tensor], k_amax: torch.Tensor, v_q: Optional[torch.Tensor],
+                      v_s: Optional[torch.Tensor], v_amax: Optional[torch.Tensor], table: torch.Tensor,
+                      starts: torch.Tensor, first: Optional[torch.Tensor] = None, bound: float = 448.0,
+                      noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keys and values of new tokens, k and v [T, H, D] (rows may lie apart, as
+    slices of a fused projection do; v None: keys alone), quantized into pages:
+    amax [pages, page_size, H] float32; q [pages, page_size, H, D] float8_e4m3fn
+    or int8, or uint8 [.., ceil(D/2)] with s [.., ceil(D/16)] (NVFP4).
+
+    Sequence b has the rows starts[b] .. starts[b + 1] - 1 and they take its
+    positions from first[b] (0 without first) on; position n lies at place
+    n % page_size of page table[b, n // page_size]. table [B, columns], starts
+    [B + 1] and first [B] are int32 device tensors. Tokens without a page are
+    skipped."""
+    lib = _lib or load_library()
+    dev = _first(k, "k", _OUT_CODES)
+    if k.dim() != 3:
+        raise ValueError("k must be 3-D [T, H, D]")
+    T, H, D = k.shape
+    fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
+    if heads != H or (v is None) != (v_q is None):
+        raise ValueError("k and v must match the cache's heads and buffers")
+    kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
+    vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
+    tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
+    st = lib.nvfp4_cache_write(kp, ks, vp, vs, _OUT_CODES[k.dtype], T, H, D, fmt, bound, pages, size, *buf,
+                               tp, B, cols, sp, fp, _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_cache_write", st)
+
+
+def nvfp4_cache_read(k: torch.Tensor, v: Optional[torch.Tensor], k_q: torch.Tensor,
+                     k_s: Optional[torch.Tensor], k_amax: torch.Tensor, v_q: Optional[torch.Tensor],
+                     v_s: Optional[torch.Tensor], v_amax: Optional[torch.Tensor], table: torch.Tensor,
+                     starts: torch.Tensor, first: Optional[torch.Tensor] = None, bound: float = 448.0,
+                     noop: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The cached tokens of each sequence as values, into rows starts[b] ..
+    starts[b + 1] - 1 of k and v [T, H, D] (bfloat16 or float32): its positions
+    from first[b] on. Arguments as nvfp4_cache_write; rows of no sequence stay as
+    they are, tokens without a page read as zeros."""
+    lib = _lib or load_library()
+    dev = _first(k, "k", _OUT_CODES)
+    if k.dim() != 3:
+        raise ValueError("k must be 3-D [T, H, D]")
+    T, H, D = k.shape
+    fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
+    if heads != H or (v is None) != (v_q is None):
+        raise ValueError("k and v must match the cache's heads and buffers")
+    kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
+    vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
+    tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
+    st = lib.nvfp4_cache_read(*buf, fmt, bound, pages, size, tp, B, cols, sp, fp, T, H, D, kp, ks, vp, vs,
+                              _OUT_CODES[k.dtype], _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        raise Nvfp4Error("nvfp4_cache_read", st)
 
 
 # --------------------------------------------------------------- conveniences

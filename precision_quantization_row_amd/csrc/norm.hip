@@ -20,86 +20,11 @@
 // (5.3 TB/s); 4097 x 2881 FP32 backward 35 + 5 us from HBM (27 + 5 from the
 // memory-side cache); one row of 8192 forward 3.9 us.
 #include "nvfp4_launch.h"
-#include "nvfp4_vec.h"
+#include "nvfp4_rows.h"
 
 #include <algorithm>
 
 namespace nvfp4 {
-
-// Sum / max over a workgroup of NT threads; every thread gets the result.
-// `red` holds NT / 64 entries; consecutive calls use different ones.
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  v = wave_sum(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NT / 64; ++i) v += red[i];
-  }
-  return v;
-}
-template <int NT>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
-  v = wave_max_u32(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0u;
-#pragma unroll
-    for (int i = 0; i < NT / 64; ++i) v = max(v, red[i]);
-  }
-  return v;
-}
-
-// Writes one lane's 8 values of a row as codes. NaN clamps to 448 in 8 bits: the
-// row's amax, NaN as well, is what carries it. c: first column (a multiple
-// of 8), n: elements of the row from c on. The lane pair (2i, 2i + 1) holds
-// one 16-element block; both lanes are active (lanes past the row hold zeros).
-__device__ __forceinline__ void write_codes(const NormArgs& p, int64_t row, int64_t c, int64_t n,
-                                            const float (&y)[8], float a, float enc8,
-                                            float s_enc) {
-  if (p.q_fmt == 1) {  // E4M3
-    float t[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = fmaxf(fminf(y[k] * enc8, kE4M3Max), -kE4M3Max);
-    uint32_t w0 = 0u, w1 = 0u;
-    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], w0, false);
-    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
-    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], w1, false);
-    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], w1, true);
-    uint8_t* q = p.q + row * p.K + c;
-    if (n >= 8) {
-      const u32x2 w = {w0, w1};
-      *reinterpret_cast<u32x2_a1*>(q) = w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) q[k] = (uint8_t)((k < 4 ? w0 : w1) >> (8 * (k & 3)));
-    }
-  } else {  // NVFP4
-    uint32_t m = 0u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(y[k]) & kAbsF32);
-    m = max(m, dpp_swap1(m));
-    uint32_t byte;
-    float enc;
-    block_scale(__uint_as_float(m), a, s_enc, p.F_inv, &byte, &enc);
-    uint32_t code = e2m1_pack8(y[0] * enc, y[1] * enc, y[2] * enc, y[3] * enc, y[4] * enc,
-                               y[5] * enc, y[6] * enc, y[7] * enc);
-    if (n > 0 && (c & 8) == 0) p.s[row * ((p.K + 15) / 16) + c / 16] = (uint8_t)byte;
-    uint8_t* q = p.q + row * ((p.K + 1) / 2) + c / 2;
-    if (n >= 8) {
-      *reinterpret_cast<u32_a1*>(q) = code;
-    } else {
-      if (n > 0) code &= (1u << (4 * n)) - 1u;  // a missing last high nibble is 0
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (2 * k < n) q[k] = (uint8_t)(code >> (8 * k));
-    }
-  }
-}
 
 // One row per workgroup, 8 * NT * V columns at most, held in registers.
 template <typename T, typename W, int NT, int V>
@@ -163,11 +88,13 @@ __global__ void __launch_bounds__(NT) norm_kernel(const NormArgs p) {
   const float a = __uint_as_float(block_max<NT>(m, redm));
   if (threadIdx.x == 0) p.row_amax[row] = a;
   if (!p.q_fmt) return;
-  const float enc8 = global_encode_scale(a, kE4M3Max), s_enc = global_encode_scale(a, p.F);
+  const float enc = global_encode_scale(a, line_top(p.q_fmt, p.F));
+  uint8_t* q = p.q + row * (p.q_fmt == FMT_E4M3 ? K : (K + 1) / 2);
+  uint8_t* s = p.s + row * ((K + 15) / 16);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int64_t c = 8 * ((int64_t)threadIdx.x + j * NT);
-    write_codes(p, row, c, K - c, h[j], a, enc8, s_enc);
+    write_codes<false>(p.q_fmt, q, s, c, K - c, h[j], a, enc, p.F_inv);
   }
 }
 
@@ -212,7 +139,9 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs p) {
   }
   const float a = __uint_as_float(block_max<NT>(m, redm));
   if (p.row_amax && threadIdx.x == 0) p.row_amax[row] = a;
-  const float enc8 = global_encode_scale(a, kE4M3Max), s_enc = global_encode_scale(a, p.F);
+  const float enc = global_encode_scale(a, line_top(p.q_fmt, p.F));
+  uint8_t* q = p.q + row * (p.q_fmt == FMT_E4M3 ? K : (K + 1) / 2);
+  uint8_t* s = p.s + row * ((K + 15) / 16);
   // every lane of a wave takes part in each turn (write_codes joins lane pairs)
   for (int64_t c0 = 8 * (int64_t)(threadIdx.x & ~63); c0 < K; c0 += step) {
     const int64_t c = c0 + 8 * (threadIdx.x & 63), n = K - c;
@@ -230,25 +159,16 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs p) {
       if (p.y_dtype == 0) store8(static_cast<uint16_t*>(p.y) + row * K + c, n, y);
       else store8(static_cast<float*>(p.y) + row * K + c, n, y);
     }
-    if (p.q_fmt) write_codes(p, row, c, n, y, a, enc8, s_enc);
+    if (p.q_fmt) write_codes<false>(p.q_fmt, q, s, c, n, y, a, enc, p.F_inv);
   }
-}
-
-// A launch holds fewer than 2^32 threads: taller inputs take several.
-template <typename F>
-static int go_rows(NormArgs a, F launch) {
-  for (int64_t r = 0; r < a.M; r += 1 << 20) {
-    a.row0 = r;
-    launch(a, (unsigned)std::min<int64_t>(a.M - r, 1 << 20));
-    if (hipGetLastError() != hipSuccess) return -3;
-  }
-  return 0;
 }
 
 template <typename T, typename W, int NT, int V>
 static int go_norm(const NormArgs& a, hipStream_t s) {
-  return go_rows(a, [s](const NormArgs& p, unsigned rows) {
-    hipLaunchKernelGGL((norm_kernel<T, W, NT, V>), dim3(rows), dim3(NT), 0, s, p);
+  return rows_in_launches(a.M, [&](int64_t r, int64_t rows) {
+    NormArgs p = a;
+    p.row0 = r;
+    hipLaunchKernelGGL((norm_kernel<T, W, NT, V>), dim3((unsigned)rows), dim3(NT), 0, s, p);
   });
 }
 
@@ -261,8 +181,10 @@ static int launch_norm_t(const NormArgs& a, hipStream_t s) {
   if (chunks <= 1024) return go_norm<T, W, 1024, 1>(a, s);
   if (chunks <= 2048) return go_norm<T, W, 1024, 2>(a, s);
   if (chunks <= 4096) return go_norm<T, W, 1024, 4>(a, s);
-  return go_rows(a, [s](const NormArgs& p, unsigned rows) {
-    hipLaunchKernelGGL((norm_long_kernel<T, W>), dim3(rows), dim3(1024), 0, s, p);
+  return rows_in_launches(a.M, [&](int64_t r, int64_t rows) {
+    NormArgs p = a;
+    p.row0 = r;
+    hipLaunchKernelGGL((norm_long_kernel<T, W>), dim3((unsigned)rows), dim3(1024), 0, s, p);
   });
 }
 
@@ -432,8 +354,10 @@ __global__ void __launch_bounds__(256) norm_dw_long_kernel(const NormBwdArgs p, 
 // strands in order. A workgroup owns 32 columns; a strand keeps 8 loads on
 // their way (64 columns, 16 strands and one load: 25 us of norm_bwd's 52 at
 // 4097 x 2881). c0: the launch's first column.
+// Columns from `split` on go to out2.
 __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int64_t P, int64_t N,
-                                                      float* out, const float* noop, int64_t c0) {
+                                                      float* out, const float* noop, int64_t c0,
+                                                      float* out2, int64_t split) {
   if (noop != nullptr && *noop == 1.0f) return;
   __shared__ float acc[32][33];
   const int col = threadIdx.x & 31, strand = threadIdx.x >> 5;
@@ -457,26 +381,17 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const float* part, int64_t
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += acc[i][col];
-    out[c] = s;
+    if (c < split) out[c] = s;
+    else out2[c - split] = s;
   }
-}
-
-// Wider inputs take several launches, too: 2^26 columns are 2^31 threads of
-// colsum_kernel (32 a column), and of norm_dw_long_kernel with 256 parts.
-template <typename F>
-static int go_columns(int64_t N, F launch) {
-  for (int64_t c = 0; c < N; c += 1 << 26) {
-    launch(c, std::min<int64_t>(N - c, 1 << 26));
-    if (hipGetLastError() != hipSuccess) return -3;
-  }
-  return 0;
 }
 
 int launch_colsum(const float* part, int64_t P, int64_t N, float* out, const float* noop,
-                  hipStream_t s) {
-  return go_columns(N, [=](int64_t c0, int64_t n) {
+                  hipStream_t s, float* out2, int64_t split) {
+  if (!out2) split = N;
+  return columns_in_launches(N, [=](int64_t c0, int64_t n) {
     hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((n + 31) / 32)), dim3(1024), 0, s, part, P, N, out,
-                       noop, c0);
+                       noop, c0, out2, split);
   });
 }
 
@@ -515,7 +430,7 @@ static int launch_norm_bwd_t(NormBwdArgs a, hipStream_t s) {
   } else {
     const int64_t P = norm_bwd_parts(a.M, a.K);
     if (a.dw) {
-      rc = go_columns(a.K, [&](int64_t c0, int64_t n) {
+      rc = columns_in_launches(a.K, [&](int64_t c0, int64_t n) {
         hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3((unsigned)((n + 2047) / 2048), (unsigned)P),
                            dim3(256), 0, s, a, c0);
       });

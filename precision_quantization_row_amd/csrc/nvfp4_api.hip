@@ -379,6 +379,200 @@ int nvfp4_act_backward(const void* dy, const void* z, int dtype, int64_t M, int6
   return launch_act_bwd(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
 }
 
+int nvfp4_int8_gemm(const int8_t* a, int a_mode, const float* a_amax, const int8_t* b, int b_mode,
+                    const float* b_amax, int64_t M, int64_t N, int64_t K, const void* bias,
+                    int bias_dtype, int act, const void* residual, void* z, void* y, int out_dtype,
+                    const float* noop, void* stream) {
+  if (!a || !a_amax || !b || !b_amax || !y) return NVFP4_ERR_ARG;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
+  if (a_mode == NVFP4_AMAX_ROWGROUP || b_mode == NVFP4_AMAX_ROWGROUP) return NVFP4_ERR_UNSUPPORTED;
+  if (a_mode != NVFP4_AMAX_TENSOR && a_mode != NVFP4_AMAX_LINE) return NVFP4_ERR_ARG;
+  if (b_mode != NVFP4_AMAX_TENSOR && b_mode != NVFP4_AMAX_LINE) return NVFP4_ERR_ARG;
+  if (act < NVFP4_ACT_NONE || act > NVFP4_ACT_SWIGLU) return NVFP4_ERR_ARG;
+  if (!valid_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype))) return NVFP4_ERR_ARG;
+  if (!int8_gemm_supported(M, N, K, act == NVFP4_ACT_SWIGLU)) return NVFP4_ERR_UNSUPPORTED;
+  GemmArgs g;
+  g.a = {reinterpret_cast<const uint8_t*>(a), nullptr, a_amax, a_mode};
+  set_factor(&g.a, 127.0f);
+  g.b = {reinterpret_cast<const uint8_t*>(b), nullptr, b_amax, b_mode};
+  set_factor(&g.b, 127.0f);
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.act = act;
+  g.bias = bias;
+  g.bias_dtype = bias_dtype;
+  g.residual = residual;
+  g.z = z;
+  g.y = y;
+  g.out_dtype = out_dtype;
+  g.noop = noop;
+  return launch_int8_gemm(g, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int nvfp4_int8_quantize(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax, int8_t* q,
+                        const float* noop, void* stream) {
+  if (!x || !row_amax || !q || M < 1 || K < 1 || M > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
+  if (!valid_dtype(in_dtype)) return NVFP4_ERR_ARG;
+  if (K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  const Int8QuantArgs a = {x,       in_dtype, M, K, row_amax, nullptr, reinterpret_cast<uint8_t*>(q),
+                           nullptr, noop};
+  return launch_int8_rows(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int nvfp4_int8_quantize_rowcol(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax,
+                               float* col_amax, int8_t* q_row, int8_t* q_col, const float* noop,
+                               void* stream) {
+  if (!x || !row_amax || !col_amax || !q_row || !q_col || M < 1 || K < 1) return NVFP4_ERR_ARG;
+  if (M > kMaxSize || K > kMaxSize || !valid_dtype(in_dtype)) return NVFP4_ERR_ARG;
+  if (M > kMaxCols || K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  const int rc = nvfp4_amax_rowcol(x, in_dtype, M, K, row_amax, col_amax, nullptr, noop, 0, stream);
+  if (rc != NVFP4_OK) return rc;
+  const Int8QuantArgs a = {x,        in_dtype, M, K, row_amax, col_amax, reinterpret_cast<uint8_t*>(q_row),
+                           reinterpret_cast<uint8_t*>(q_col), noop};
+  return launch_int8_rowcol(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int nvfp4_layernorm(const void* x, const void* residual, int in_dtype, const void* weight,
+                    const void* bias, int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y,
+                    int y_dtype, float* mean, float* rstd, int q_fmt, uint8_t* q, uint8_t* s,
+                    float* row_amax, float bound, const float* noop, void* stream) {
+  if (!x || !weight || M < 1 || K < 1 || M > kMaxSize || K > kMaxSize) return NVFP4_ERR_ARG;
+  if (!valid_dtype(in_dtype) || !valid_dtype(w_dtype)) return NVFP4_ERR_ARG;
+  if (!(isfinite(eps) && eps >= 0.0f)) return NVFP4_ERR_ARG;
+  if (y && !valid_dtype(y_dtype)) return NVFP4_ERR_ARG;
+  if (q_fmt < NVFP4_FMT_NONE || q_fmt > NVFP4_FMT_INT8) return NVFP4_ERR_ARG;
+  if ((q_fmt != NVFP4_FMT_NONE) != (q != nullptr)) return NVFP4_ERR_ARG;
+  if ((q_fmt == NVFP4_FMT_NVFP4) != (s != nullptr)) return NVFP4_ERR_ARG;
+  if (q && !row_amax) return NVFP4_ERR_ARG;
+  if (q_fmt == NVFP4_FMT_NVFP4 && !valid_bound(bound)) return NVFP4_ERR_ARG;
+  if (!h && !y && !mean && !rstd && !row_amax) return NVFP4_ERR_ARG;
+  if (K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  LayerNormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.b = bias;
+  a.in_dtype = in_dtype;
+  a.w_dtype = w_dtype;
+  a.M = M;
+  a.K = K;
+  a.eps = eps;
+  a.h = h;
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.q_fmt = q_fmt;
+  a.q = q;
+  a.s = s;
+  a.row_amax = row_amax;
+  a.F = q_fmt == NVFP4_FMT_NVFP4 ? bound * 6.0f : 1.0f;
+  a.F_inv = 1.0f / a.F;
+  a.noop = noop;
+  return launch_layernorm(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int64_t nvfp4_layernorm_backward_workspace(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || M > kMaxSize || K > kMaxCols) return 0;
+  return 8 * layernorm_bwd_parts(M, K) * K;
+}
+
+int nvfp4_layernorm_backward(const void* dy, const void* h, int in_dtype, const void* weight,
+                             int w_dtype, const float* mean, const float* rstd, const void* dres,
+                             int64_t M, int64_t K, void* dx, float* dweight, float* dbias,
+                             void* workspace, int64_t workspace_bytes, const float* noop,
+                             void* stream) {
+  if (!dy || !h || !weight || !mean || !rstd || !dx || M < 1 || K < 1 || M > kMaxSize || K > kMaxSize)
+    return NVFP4_ERR_ARG;
+  if (!valid_dtype(in_dtype) || !valid_dtype(w_dtype)) return NVFP4_ERR_ARG;
+  if (K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
+  if ((dweight || dbias) &&
+      (!workspace || workspace_bytes < nvfp4_layernorm_backward_workspace(M, K) ||
+       (reinterpret_cast<uintptr_t>(workspace) & 15) != 0))
+    return NVFP4_ERR_ARG;
+  const LayerNormBwdArgs a = {dy, h, weight, dres,  in_dtype, w_dtype, mean, rstd, M, K,
+                              dx, dweight, dbias, static_cast<float*>(workspace), noop};
+  return launch_layernorm_bwd(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+// What the two directions of the cache have in common. A bad request's status, or
+// NVFP4_OK with `a` filled but for the rows' pointers.
+static int cache_args(CacheArgs* a, int dtype, int64_t T, int64_t H, int64_t D, int64_t k_stride,
+                      int64_t v_stride, int fmt, float bound, int64_t pages, int64_t page_size,
+                      const void* k_q, const void* k_s, const float* k_amax, const void* v_q,
+                      const void* v_s, const float* v_amax, const int32_t* table, int64_t B,
+                      int64_t table_cols, const int32_t* starts, const int32_t* first,
+                      const float* noop) {
+  if (!k_q || !k_amax || !table || !starts || !valid_dtype(dtype)) return NVFP4_ERR_ARG;
+  if (T < 1 || H < 1 || D < 1 || B < 1 || table_cols < 1 || pages < 1 || page_size < 1) return NVFP4_ERR_ARG;
+  for (int64_t n : {T, H, D, B, table_cols, pages, page_size, k_stride, v_stride})
+    if (n > kMaxSize || n < -kMaxSize) return NVFP4_ERR_ARG;
+  if (fmt != NVFP4_FMT_E4M3 && fmt != NVFP4_FMT_NVFP4 && fmt != NVFP4_FMT_INT8) return NVFP4_ERR_ARG;
+  if (fmt == NVFP4_FMT_NVFP4 && !valid_bound(bound)) return NVFP4_ERR_ARG;
+  if ((fmt == NVFP4_FMT_NVFP4) != (k_s != nullptr)) return NVFP4_ERR_ARG;
+  if ((v_q != nullptr) != (v_amax != nullptr)) return NVFP4_ERR_ARG;
+  if ((v_q && fmt == NVFP4_FMT_NVFP4) != (v_s != nullptr)) return NVFP4_ERR_ARG;
+  if (D > 1024 || H > 65535 || T > 0x7FFFFFFF || B > 0x7FFFFFFE) return NVFP4_ERR_UNSUPPORTED;
+  a->stride[0] = k_stride;
+  a->stride[1] = v_stride;
+  a->dtype = dtype;
+  a->T = T;
+  a->H = H;
+  a->D = D;
+  a->fmt = fmt;
+  a->F = fmt == NVFP4_FMT_NVFP4 ? bound * 6.0f : 1.0f;
+  a->F_inv = 1.0f / a->F;
+  a->pages = pages;
+  a->page_size = page_size;
+  a->q[0] = static_cast<uint8_t*>(const_cast<void*>(k_q));
+  a->q[1] = static_cast<uint8_t*>(const_cast<void*>(v_q));
+  a->s[0] = static_cast<uint8_t*>(const_cast<void*>(k_s));
+  a->s[1] = static_cast<uint8_t*>(const_cast<void*>(v_s));
+  a->amax[0] = const_cast<float*>(k_amax);
+  a->amax[1] = const_cast<float*>(v_amax);
+  a->table = table;
+  a->B = B;
+  a->cols = table_cols;
+  a->starts = starts;
+  a->first = first;
+  a->noop = noop;
+  return NVFP4_OK;
+}
+
+int nvfp4_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int in_dtype,
+                      int64_t T, int64_t H, int64_t D, int fmt, float bound, int64_t pages,
+                      int64_t page_size, void* k_q, void* k_s, float* k_amax, void* v_q, void* v_s,
+                      float* v_amax, const int32_t* table, int64_t B, int64_t table_cols,
+                      const int32_t* starts, const int32_t* first, const float* noop, void* stream) {
+  if (!k || (v != nullptr) != (v_q != nullptr) || k_stride < 0 || (v && v_stride < 0)) return NVFP4_ERR_ARG;
+  CacheArgs a;
+  const int rc = cache_args(&a, in_dtype, T, H, D, k_stride, v ? v_stride : 0, fmt, bound, pages, page_size,
+                            k_q, k_s, k_amax, v_q, v_s, v_amax, table, B, table_cols, starts, first, noop);
+  if (rc != NVFP4_OK) return rc;
+  a.src[0] = k;
+  a.src[1] = v;
+  return launch_cache_write(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
+int nvfp4_cache_read(const void* k_q, const void* k_s, const float* k_amax, const void* v_q,
+                     const void* v_s, const float* v_amax, int fmt, float bound, int64_t pages,
+                     int64_t page_size, const int32_t* table, int64_t B, int64_t table_cols,
+                     const int32_t* starts, const int32_t* first, int64_t T, int64_t H, int64_t D,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride, int out_dtype,
+                     const float* noop, void* stream) {
+  if (!k || (v != nullptr) != (v_q != nullptr)) return NVFP4_ERR_ARG;
+  CacheArgs a;
+  const int rc = cache_args(&a, out_dtype, T, H, D, k_stride, v ? v_stride : 0, fmt, bound, pages, page_size,
+                            k_q, k_s, k_amax, v_q, v_s, v_amax, table, B, table_cols, starts, first, noop);
+  if (rc != NVFP4_OK) return rc;
+  // rows that overlap would be written by two tokens
+  if (T > 1 && (k_stride < H * D || (v && v_stride < H * D))) return NVFP4_ERR_ARG;
+  a.dst[0] = k;
+  a.dst[1] = v;
+  return launch_cache_read(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;
+}
+
 int nvfp4_rmsnorm(const void* x, const void* residual, int in_dtype, const void* weight,
                   int w_dtype, float eps, int64_t M, int64_t K, void* h, void* y, int y_dtype,
                   float* rstd, int q_fmt, uint8_t* q, uint8_t* s, float* row_amax, float bound,

@@ -109,9 +109,76 @@ struct NormBwdArgs {
 int64_t norm_bwd_parts(int64_t M, int64_t K);
 int launch_norm_bwd(const NormBwdArgs& a, hipStream_t s);
 
-// sums over the rows of part [P][N], in a fixed order
+// sums over the rows of part [P][N], in a fixed order; with out2, columns from
+// `split` on go there
 int launch_colsum(const float* part, int64_t P, int64_t N, float* out, const float* noop,
-                  hipStream_t s);
+                  hipStream_t s, float* out2 = nullptr, int64_t split = 0);
+
+// layer norm (layernorm.hip)
+struct LayerNormArgs {
+  const void *x, *residual, *w, *b;
+  int in_dtype, w_dtype;  // 0 BF16, 1 FP32; b has w's type
+  int64_t M, K;
+  float eps;
+  void* h;
+  void* y;
+  int y_dtype;
+  float *mean, *rstd;
+  int q_fmt;  // 0 none, 1 E4M3, 2 NVFP4, 3 INT8
+  uint8_t *q, *s;
+  float* row_amax;
+  float F, F_inv;
+  const float* noop;
+  int64_t row0 = 0;
+};
+int launch_layernorm(const LayerNormArgs& a, hipStream_t s);
+
+struct LayerNormBwdArgs {
+  const void *dy, *h, *w, *dres;
+  int in_dtype, w_dtype;
+  const float *mean, *rstd;
+  int64_t M, K;
+  void* dx;
+  float *dw, *db;
+  float* part;  // [layernorm_bwd_parts(M, K)][K, or 2 K with dw and db]
+  const float* noop;
+};
+int64_t layernorm_bwd_parts(int64_t M, int64_t K);
+int launch_layernorm_bwd(const LayerNormBwdArgs& a, hipStream_t s);
+
+// 8-bit integer lines (int8_quant.hip)
+struct Int8QuantArgs {
+  const void* x;
+  int in_dtype;
+  int64_t M, K;
+  float *row_amax, *col_amax;
+  uint8_t *q_row, *q_col;
+  const float* noop;
+  int64_t row0 = 0;
+};
+int launch_int8_rows(const Int8QuantArgs& a, hipStream_t s);     // row_amax and q_row
+int launch_int8_rowcol(const Int8QuantArgs& a, hipStream_t s);   // both copies, from the amaxes
+
+// pages of quantized lines (cache.hip); [0]: keys, [1]: values (q[1] NULL: none)
+struct CacheArgs {
+  const void* src[2];  // write: [T][H][D], `stride` elements from token to token
+  void* dst[2];        // read
+  int64_t stride[2];
+  int dtype;           // of src or dst
+  int64_t T, H, D;
+  int fmt;
+  float F, F_inv;
+  int64_t pages, page_size;
+  uint8_t *q[2], *s[2];
+  float* amax[2];
+  const int32_t* table;  // [B][cols]
+  int64_t B, cols;
+  const int32_t *starts, *first;  // [B + 1], [B] or NULL
+  const float* noop;
+  int64_t t0 = 0;
+};
+int launch_cache_write(const CacheArgs& a, hipStream_t s);
+int launch_cache_read(const CacheArgs& a, hipStream_t s);
 
 // backward of the product's epilogue (act.hip)
 struct ActBwdArgs {
@@ -153,5 +220,13 @@ int launch_gemm(const GemmArgs& a, hipStream_t s);
 int64_t gemm_tiles(int64_t M, int64_t N, bool gated);  // workgroups of the tile kernel
 void launch_gemm_tile(const GemmArgs& a, hipStream_t s);
 void launch_gemm_rows(const GemmArgs& a, hipStream_t s);
+
+
+// product of 8-bit integer lines (int8_gemm.hip); a GemmOperand without block
+// scales, its factor 1 / 127
+bool int8_gemm_supported(int64_t M, int64_t N, int64_t K, bool gated);
+int launch_int8_gemm(const GemmArgs& a, hipStream_t s);
+void launch_int8_tile(const GemmArgs& a, hipStream_t s);
+void launch_int8_rows_gemm(const GemmArgs& a, hipStream_t s);
 
 }  // namespace nvfp4

@@ -1,0 +1,197 @@
+// nvfp4_rows.h -- rows (lines) held by groups of lanes, 8 elements a lane and
+// run: reductions over the group and the codes of its elements (gfx950).
+#pragma once
+
+#include "nvfp4_vec.h"
+
+namespace nvfp4 {
+
+enum { FMT_NONE = 0, FMT_E4M3 = 1, FMT_NVFP4 = 2, FMT_INT8 = 3 };
+constexpr float kInt8Max = 127.0f;
+
+// Sum / max over a workgroup of NT threads; every thread gets the result.
+// `red` holds NT / 64 entries; consecutive calls use different ones.
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) v += red[i];
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = wave_max_u32(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0u;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) v = max(v, red[i]);
+  }
+  return v;
+}
+
+// The same over a row's L lanes: a power of two up to 64 (rows side by side in
+// a wave; `red` unused), or a whole workgroup of L threads.
+template <int L>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  if constexpr (L <= 64) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+  } else {
+    return block_sum<L>(v, red);
+  }
+}
+// two sums at once (red: 2 L / 64 entries)
+template <int L>
+__device__ __forceinline__ void row_sum2(float& u, float& v, float* red) {
+#pragma unroll
+  for (int o = (L < 64 ? L : 64) / 2; o > 0; o >>= 1) {
+    u += __shfl_xor(u, o);
+    v += __shfl_xor(v, o);
+  }
+  if constexpr (L > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      red[2 * (threadIdx.x >> 6)] = u;
+      red[2 * (threadIdx.x >> 6) + 1] = v;
+    }
+    __syncthreads();
+    u = v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L / 64; ++i) {
+      u += red[2 * i];
+      v += red[2 * i + 1];
+    }
+  }
+}
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  if constexpr (L <= 64) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
+  } else {
+    return block_max<L>(v, red);
+  }
+}
+
+// The second-level amax bits of 8 values joined to m. A NaN's bits lie above
+// every number's, so a line that holds one has a NaN amax.
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & kAbsF32);
+  return m;
+}
+
+// 8 values as E4M3 bytes: RN(v enc) clamped to 448 with the sign kept, to nearest even
+__device__ __forceinline__ u32x2 pack8_e4m3(const float (&v)[8], float enc) {
+  float t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = fmaxf(fminf(v[k] * enc, kE4M3Max), -kE4M3Max);
+  uint32_t w0 = 0u, w1 = 0u;
+  w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], w0, false);
+  w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
+  w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], w1, false);
+  w1 = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], w1, true);
+  return u32x2{w0, w1};
+}
+
+// The integer nearest to RN(v enc), halves to the even one, clamped to +-127, in
+// the low byte. 1.5 * 2^23 has steps of one and is even: adding it rounds so,
+// and the sum's low byte is the integer's two's complement.
+__device__ __forceinline__ uint32_t int8_code(float v, float enc) {
+  return __float_as_uint(fmaxf(fminf(v * enc, kInt8Max), -kInt8Max) + 12582912.0f);
+}
+// the low bytes of four dwords, a first
+__device__ __forceinline__ uint32_t pack4_low(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0C0C0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x0C0C0400u);
+  return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+}
+__device__ __forceinline__ u32x2 pack8_int8(const float (&v)[8], float enc) {
+  uint32_t t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = int8_code(v[k], enc);
+  return u32x2{pack4_low(t[0], t[1], t[2], t[3]), pack4_low(t[4], t[5], t[6], t[7])};
+}
+
+// 8 bytes, or the first n of them
+__device__ __forceinline__ void store8_bytes(uint8_t* q, int64_t n, u32x2 w) {
+  if (n >= 8) {
+    *reinterpret_cast<u32x2_a1*>(q) = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) q[k] = (uint8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+  }
+}
+
+// What a format maps a line's amax to, before its block scales if it has any.
+__device__ __forceinline__ float line_top(int fmt, float F) {
+  return fmt == FMT_E4M3 ? kE4M3Max : fmt == FMT_INT8 ? kInt8Max : F;
+}
+
+// Writes one lane's 8 values of a line as codes. NaN clamps to the top code in 8
+// bits: the line's amax, NaN as well, is what carries it. q, s: the line's
+// first code and block scale; c: first element (a multiple of 8), n: elements
+// of the line from c on; a: the line's amax, enc: its encode scale. The lane
+// pair (2i, 2i + 1) holds one 16-element block; both lanes are active (lanes
+// past the line hold zeros). I8: the format may be INT8.
+template <bool I8>
+__device__ __forceinline__ void write_codes(int fmt, uint8_t* q, uint8_t* s, int64_t c, int64_t n,
+                                            const float (&y)[8], float a, float enc, float F_inv) {
+  if (I8 && fmt == FMT_INT8) {
+    store8_bytes(q + c, n, pack8_int8(y, enc));
+  } else if (fmt == FMT_E4M3) {
+    store8_bytes(q + c, n, pack8_e4m3(y, enc));
+  } else {  // NVFP4
+    uint32_t m = amax8(y, 0u);
+    m = max(m, dpp_swap1(m));
+    uint32_t byte;
+    float e;
+    block_scale(__uint_as_float(m), a, enc, F_inv, &byte, &e);
+    uint32_t code = e2m1_pack8(y[0] * e, y[1] * e, y[2] * e, y[3] * e, y[4] * e, y[5] * e, y[6] * e,
+                               y[7] * e);
+    if (n > 0 && (c & 8) == 0) s[c / 16] = (uint8_t)byte;
+    q += c / 2;
+    if (n >= 8) {
+      *reinterpret_cast<u32_a1*>(q) = code;
+    } else {
+      if (n > 0) code &= (1u << (4 * n)) - 1u;  // a missing last high nibble is 0
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (2 * k < n) q[k] = (uint8_t)(code >> (8 * k));
+    }
+  }
+}
+
+// A launch holds fewer than 2^32 threads: taller inputs take several.
+// launch(first row, rows)
+template <typename F>
+static int rows_in_launches(int64_t M, F launch) {
+  for (int64_t r = 0; r < M; r += 1 << 20) {
+    launch(r, M - r < (1 << 20) ? M - r : (int64_t)(1 << 20));
+    if (hipGetLastError() != hipSuccess) return -3;
+  }
+  return 0;
+}
+
+// Wider inputs take several launches, too: 2^26 columns are 2^31 threads at 32
+// threads a column, and with 256 parts at 8 columns a thread.
+// launch(first column, columns)
+template <typename F>
+static int columns_in_launches(int64_t N, F launch) {
+  for (int64_t c = 0; c < N; c += 1 << 26) {
+    launch(c, N - c < (1 << 26) ? N - c : (int64_t)(1 << 26));
+    if (hipGetLastError() != hipSuccess) return -3;
+  }
+  return 0;
+}
+
+}  // namespace nvfp4
