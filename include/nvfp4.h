@@ -502,7 +502,7 @@ int nvfp4_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_
  * sequence as values, in rows starts[b] .. starts[b + 1] - 1 of k and v: the
  * arguments of nvfp4_cache_write the other way round.
  *   NVFP4: RN(e2m1(code) RN(RN(e4m3(byte) a) F_inv)), as nvfp4_dequantize;
- *   E4M3:  RN(byte RN(a / 448));  INT8: RN(byte RN(a / 127));
+ *   E4M3:  RN(byte RN(a RN(1 / 448)));  INT8: RN(byte RN(a RN(1 / 127)));
  *   out_dtype BF16 rounds that FP32 value once more
  *   k, v [T] rows, k_stride and v_stride elements (>= H D) apart
  * Rows of no token are left as they are. A token without a page (as above) reads

@@ -16,12 +16,13 @@ Layouts (row-major, packed, no pitch):
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
 import torch
 
-from .build import library_path
+from .build import calls_path, library_path
 
 NVFP4_OK = 0
 NVFP4_ERR_ARG = -1
@@ -638,6 +639,21 @@ def nvfp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
 
 
 # -------------------------------- 8-bit integers, layer norm, quantized cache
+# A decode step's kernels run for a few us: _calls.so checks the tensors and calls
+# the library. Where it finds something amiss it returns None, and the checks
+# here, which are the same, say what.
+_short = None
+
+
+def _load_short():
+    global _short
+    load_library()
+    if not os.path.exists(calls_path()):
+        raise ImportError(f"{calls_path()} is missing: build it with __graft_entry__.build()")
+    _short = importlib.import_module("._calls", __name__)
+    return _short
+
+
 _I8 = (torch.int8,)
 _I32 = (torch.int32,)
 
@@ -646,14 +662,17 @@ def nvfp4_int8_quantize(x: torch.Tensor, row_amax: torch.Tensor, q: torch.Tensor
                         noop: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows of x [M, K] as 8-bit integers: row_amax [M] float32 and q [M, K] int8,
     both written; value = q * row_amax / 127."""
-    lib = _lib or load_library()
-    dev = _first(x, "x", _OUT_CODES)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D [M, K]")
-    M, K = x.shape
-    st = lib.nvfp4_int8_quantize(_arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
-                                 _arg(row_amax, "row_amax", _F32, M, dev), _arg(q, "q", _I8, M * K, dev),
-                                 _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    st = (_short or _load_short()).int8_quantize(x, row_amax, q, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(x, "x", _OUT_CODES)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D [M, K]")
+        M, K = x.shape
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_int8_quantize(_arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
+                                         _arg(row_amax, "row_amax", _F32, M, dev), _arg(q, "q", _I8, M * K, dev),
+                                         _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_int8_quantize", st)
 
@@ -663,16 +682,19 @@ def nvfp4_int8_quantize_rowcol(x: torch.Tensor, row_amax: torch.Tensor, col_amax
                                noop: Optional[torch.Tensor] = None, stream=None) -> None:
     """Both copies of x [M, K] as 8-bit integers: row_amax [M] and q_row [M, K],
     col_amax [K] and q_col [K, M] (the transpose), all written."""
-    lib = _lib or load_library()
-    dev = _first(x, "x", _OUT_CODES)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D [M, K]")
-    M, K = x.shape
-    st = lib.nvfp4_int8_quantize_rowcol(
-        _arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
-        _arg(row_amax, "row_amax", _F32, M, dev), _arg(col_amax, "col_amax", _F32, K, dev),
-        _arg(q_row, "q_row", _I8, M * K, dev), _arg(q_col, "q_col", _I8, M * K, dev),
-        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    st = (_short or _load_short()).int8_quantize_rowcol(x, row_amax, col_amax, q_row, q_col, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(x, "x", _OUT_CODES)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D [M, K]")
+        M, K = x.shape
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_int8_quantize_rowcol(
+                _arg(x, "x", (x.dtype,), M * K, dev), _OUT_CODES[x.dtype], M, K,
+                _arg(row_amax, "row_amax", _F32, M, dev), _arg(col_amax, "col_amax", _F32, K, dev),
+                _arg(q_row, "q_row", _I8, M * K, dev), _arg(q_col, "q_col", _I8, M * K, dev),
+                _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_int8_quantize_rowcol", st)
 
@@ -686,23 +708,27 @@ def nvfp4_int8_gemm(a: torch.Tensor, a_mode: int, a_amax: torch.Tensor, b: torch
     b [N, K] (2 N lines for NVFP4_ACT_SWIGLU: gate lines, then up lines), each
     line with its amax (or one for all, NVFP4_AMAX_TENSOR). z, y, residual and
     bias as in nvfp4_gemm."""
-    lib = _lib or load_library()
-    dev = _first(a, "a", _I8)
-    out = _OUT_CODES.get(getattr(y, "dtype", None))
-    if out is None:
-        raise TypeError("y must be a bfloat16 or float32 tensor")
-    NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
-    same = (y.dtype,)
-    st = lib.nvfp4_int8_gemm(
-        _arg(a, "a", _I8, M * K, dev), a_mode,
-        _arg(a_amax, "a_amax", _F32, M if a_mode == NVFP4_AMAX_LINE else 1, dev),
-        _arg(b, "b", _I8, NB * K, dev), b_mode,
-        _arg(b_amax, "b_amax", _F32, NB if b_mode == NVFP4_AMAX_LINE else 1, dev),
-        M, N, K, _arg(bias, "bias", _OUT_CODES, NB, dev),
-        0 if bias is None else _OUT_CODES[bias.dtype], act,
-        _arg(residual, "residual", same, M * N, dev), _arg(z, "z", same, M * NB, dev),
-        _arg(y, "y", same, M * N, dev), out, _arg(noop, "noop", _F32, 1, dev),
-        _raw_stream(stream, dev))
+    st = (_short or _load_short()).int8_gemm(a, a_mode, a_amax, b, b_mode, b_amax, M, N, K, y, bias, act,
+                                             residual, z, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(a, "a", _I8)
+        out = _OUT_CODES.get(getattr(y, "dtype", None))
+        if out is None:
+            raise TypeError("y must be a bfloat16 or float32 tensor")
+        NB = 2 * N if act == NVFP4_ACT_SWIGLU else N
+        same = (y.dtype,)
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_int8_gemm(
+                _arg(a, "a", _I8, M * K, dev), a_mode,
+                _arg(a_amax, "a_amax", _F32, M if a_mode == NVFP4_AMAX_LINE else 1, dev),
+                _arg(b, "b", _I8, NB * K, dev), b_mode,
+                _arg(b_amax, "b_amax", _F32, NB if b_mode == NVFP4_AMAX_LINE else 1, dev),
+                M, N, K, _arg(bias, "bias", _OUT_CODES, NB, dev),
+                0 if bias is None else _OUT_CODES[bias.dtype], act,
+                _arg(residual, "residual", same, M * N, dev), _arg(z, "z", same, M * NB, dev),
+                _arg(y, "y", same, M * N, dev), out, _arg(noop, "noop", _F32, 1, dev),
+                _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_int8_gemm", st)
 
@@ -721,26 +747,30 @@ def nvfp4_layernorm(x: torch.Tensor, weight: torch.Tensor, eps: float, bias: Opt
     uint8 [M, ceil(K/2)] with s [M, ceil(K/16)] (NVFP4). bias has weight's dtype.
     Outputs not given are not written; mean and rstd are what
     nvfp4_layernorm_backward takes."""
-    lib = _lib or load_library()
-    dev = _first(x, "x", _OUT_CODES)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D [M, K]")
-    M, K = x.shape
-    same, wtype = (x.dtype,), getattr(weight, "dtype", None)
-    fmt, qn = NVFP4_FMT_NONE, 0
-    if q is not None:
-        fmt = _NORM_FORMATS.get(q.dtype, NVFP4_FMT_NVFP4)
-        qn = M * ((K + 1) // 2) if fmt == NVFP4_FMT_NVFP4 else M * K
-    st = lib.nvfp4_layernorm(
-        _arg(x, "x", same, M * K, dev), _arg(residual, "residual", same, M * K, dev),
-        _OUT_CODES[x.dtype], _arg(weight, "weight", _OUT_CODES, K, dev), _arg(bias, "bias", (wtype,), K, dev),
-        _OUT_CODES.get(wtype, -1), eps, M, K, _arg(h, "h", same, M * K, dev),
-        _arg(y, "y", _OUT_CODES, M * K, dev), 0 if y is None else _OUT_CODES[y.dtype],
-        _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev), fmt,
-        _arg(q, "q", tuple(_NORM_FORMATS), qn, dev),
-        _arg(s, "s", _SCALE_DTYPES, M * ((K + 15) // 16), dev),
-        _arg(row_amax, "row_amax", _F32, M, dev), bound, _arg(noop, "noop", _F32, 1, dev),
-        _raw_stream(stream, dev))
+    st = (_short or _load_short()).layernorm(x, weight, eps, bias, residual, h, y, mean, rstd, q, s, row_amax,
+                                             bound, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(x, "x", _OUT_CODES)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D [M, K]")
+        M, K = x.shape
+        same, wtype = (x.dtype,), getattr(weight, "dtype", None)
+        fmt, qn = NVFP4_FMT_NONE, 0
+        if q is not None:
+            fmt = _NORM_FORMATS.get(q.dtype, NVFP4_FMT_NVFP4)
+            qn = M * ((K + 1) // 2) if fmt == NVFP4_FMT_NVFP4 else M * K
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_layernorm(
+                _arg(x, "x", same, M * K, dev), _arg(residual, "residual", same, M * K, dev),
+                _OUT_CODES[x.dtype], _arg(weight, "weight", _OUT_CODES, K, dev), _arg(bias, "bias", (wtype,), K, dev),
+                _OUT_CODES.get(wtype, -1), eps, M, K, _arg(h, "h", same, M * K, dev),
+                _arg(y, "y", _OUT_CODES, M * K, dev), 0 if y is None else _OUT_CODES[y.dtype],
+                _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev), fmt,
+                _arg(q, "q", tuple(_NORM_FORMATS), qn, dev),
+                _arg(s, "s", _SCALE_DTYPES, M * ((K + 15) // 16), dev),
+                _arg(row_amax, "row_amax", _F32, M, dev), bound, _arg(noop, "noop", _F32, 1, dev),
+                _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_layernorm", st)
 
@@ -760,22 +790,26 @@ def nvfp4_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
     """dx [M, K], dweight [K] and dbias [K] (float32) of nvfp4_layernorm from
     dy [M, K] and the saved h, mean and rstd; dres, the gradient that reaches h by
     other ways, is added to dx."""
-    lib = _lib or load_library()
-    dev = _first(dy, "dy", _OUT_CODES)
-    if dy.dim() != 2:
-        raise ValueError("dy must be 2-D [M, K]")
-    M, K = dy.shape
-    same = (dy.dtype,)
-    sums = dweight is not None or dbias is not None
-    need = lib.nvfp4_layernorm_backward_workspace(M, K) if sums else 0
-    ws, wp, wb = _workspace(workspace, need, dev, stream)
-    st = lib.nvfp4_layernorm_backward(
-        _arg(dy, "dy", same, M * K, dev), _arg(h, "h", same, M * K, dev), _OUT_CODES[dy.dtype],
-        _arg(weight, "weight", _OUT_CODES, K, dev), _OUT_CODES.get(getattr(weight, "dtype", None), -1),
-        _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev),
-        _arg(dres, "dres", same, M * K, dev), M, K, _arg(dx, "dx", same, M * K, dev),
-        _arg(dweight, "dweight", _F32, K, dev), _arg(dbias, "dbias", _F32, K, dev), wp, wb,
-        _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    st = (_short or _load_short()).layernorm_backward(dy, h, weight, mean, rstd, dx, dweight, dbias, dres,
+                                                      workspace, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(dy, "dy", _OUT_CODES)
+        if dy.dim() != 2:
+            raise ValueError("dy must be 2-D [M, K]")
+        M, K = dy.shape
+        same = (dy.dtype,)
+        sums = dweight is not None or dbias is not None
+        need = lib.nvfp4_layernorm_backward_workspace(M, K) if sums else 0
+        ws, wp, wb = _workspace(workspace, need, dev, stream)
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_layernorm_backward(
+                _arg(dy, "dy", same, M * K, dev), _arg(h, "h", same, M * K, dev), _OUT_CODES[dy.dtype],
+                _arg(weight, "weight", _OUT_CODES, K, dev), _OUT_CODES.get(getattr(weight, "dtype", None), -1),
+                _arg(mean, "mean", _F32, M, dev), _arg(rstd, "rstd", _F32, M, dev),
+                _arg(dres, "dres", same, M * K, dev), M, K, _arg(dx, "dx", same, M * K, dev),
+                _arg(dweight, "dweight", _F32, K, dev), _arg(dbias, "dbias", _F32, K, dev), wp, wb,
+                _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_layernorm_backward", st)
 
@@ -848,19 +882,23 @@ def nvfp4_cache_write(k: torch.Tensor, v: Optional[torch.Tensor], k_q: torch.Ten
     n % page_size of page table[b, n // page_size]. table [B, columns], starts
     [B + 1] and first [B] are int32 device tensors. Tokens without a page are
     skipped."""
-    lib = _lib or load_library()
-    dev = _first(k, "k", _OUT_CODES)
-    if k.dim() != 3:
-        raise ValueError("k must be 3-D [T, H, D]")
-    T, H, D = k.shape
-    fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
-    if heads != H or (v is None) != (v_q is None):
-        raise ValueError("k and v must match the cache's heads and buffers")
-    kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
-    vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
-    tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
-    st = lib.nvfp4_cache_write(kp, ks, vp, vs, _OUT_CODES[k.dtype], T, H, D, fmt, bound, pages, size, *buf,
-                               tp, B, cols, sp, fp, _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    st = (_short or _load_short()).cache_write(k, v, k_q, k_s, k_amax, v_q, v_s, v_amax, table, starts, first,
+                                               bound, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(k, "k", _OUT_CODES)
+        if k.dim() != 3:
+            raise ValueError("k must be 3-D [T, H, D]")
+        T, H, D = k.shape
+        fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
+        if heads != H or (v is None) != (v_q is None):
+            raise ValueError("k and v must match the cache's heads and buffers")
+        kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
+        vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
+        tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_cache_write(kp, ks, vp, vs, _OUT_CODES[k.dtype], T, H, D, fmt, bound, pages, size, *buf,
+                                       tp, B, cols, sp, fp, _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_cache_write", st)
 
@@ -874,19 +912,23 @@ def nvfp4_cache_read(k: torch.Tensor, v: Optional[torch.Tensor], k_q: torch.Tens
     starts[b + 1] - 1 of k and v [T, H, D] (bfloat16 or float32): its positions
     from first[b] on. Arguments as nvfp4_cache_write; rows of no sequence stay as
     they are, tokens without a page read as zeros."""
-    lib = _lib or load_library()
-    dev = _first(k, "k", _OUT_CODES)
-    if k.dim() != 3:
-        raise ValueError("k must be 3-D [T, H, D]")
-    T, H, D = k.shape
-    fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
-    if heads != H or (v is None) != (v_q is None):
-        raise ValueError("k and v must match the cache's heads and buffers")
-    kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
-    vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
-    tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
-    st = lib.nvfp4_cache_read(*buf, fmt, bound, pages, size, tp, B, cols, sp, fp, T, H, D, kp, ks, vp, vs,
-                              _OUT_CODES[k.dtype], _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
+    st = (_short or _load_short()).cache_read(k, v, k_q, k_s, k_amax, v_q, v_s, v_amax, table, starts, first,
+                                              bound, noop, stream)
+    if st is None:
+        lib = load_library()
+        dev = _first(k, "k", _OUT_CODES)
+        if k.dim() != 3:
+            raise ValueError("k must be 3-D [T, H, D]")
+        T, H, D = k.shape
+        fmt, pages, size, heads, buf = _cache(k_q, k_s, k_amax, v_q, v_s, v_amax, D, dev)
+        if heads != H or (v is None) != (v_q is None):
+            raise ValueError("k and v must match the cache's heads and buffers")
+        kp, ks = _rows(k, "k", (k.dtype,), k.shape, dev)
+        vp, vs = _rows(v, "v", (k.dtype,), k.shape, dev)
+        tp, B, cols, sp, fp = _sequences(table, starts, first, dev)
+        with torch.cuda.device(dev):
+            st = lib.nvfp4_cache_read(*buf, fmt, bound, pages, size, tp, B, cols, sp, fp, T, H, D, kp, ks, vp, vs,
+                                      _OUT_CODES[k.dtype], _arg(noop, "noop", _F32, 1, dev), _raw_stream(stream, dev))
     if st:
         raise Nvfp4Error("nvfp4_cache_read", st)
 

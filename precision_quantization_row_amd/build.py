@@ -1,6 +1,8 @@
 """Build libnvfp4.so (the HIP kernels and the C ABI) in-tree for gfx950, and
 the reference streaming kernels bench.py measures the HBM ceiling with
-(bench_ref/libstream_ref.so, not part of the library).
+(bench_ref/libstream_ref.so, not part of the library); and _calls.so, the short
+way from torch tensors to the library's calls (host code, by g++ with Python's and
+torch's headers).
 
 hipcc compiles every .hip source under csrc/ (several at a time) into one
 shared library next to this file. Flags:
@@ -60,6 +62,32 @@ def _hipcc(sources, out, includes, verbose):
     return out
 
 
+def calls_path() -> str:
+    """The in-tree _calls.so."""
+    return os.path.join(HERE, "_calls.so")
+
+
+def build_calls(verbose: bool = False) -> str:
+    """After build_library: it links against libnvfp4.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    out = calls_path()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *cpp_extension.include_paths()]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(x for i in inc for x in ("-isystem", i)),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", os.path.join(HERE, "binding", "calls.cpp"),
+           "-o", out + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", HERE, "-l:libnvfp4.so",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build_library(verbose: bool = False, out: str = None, csrc: str = CSRC) -> str:
     return _hipcc(sorted(glob.glob(os.path.join(csrc, "*.hip"))),
                   out or library_path(), [os.path.join(ROOT, "include"), csrc], verbose)
@@ -71,4 +99,5 @@ def build_stream_ref(verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_calls(verbose=True))
     print(build_stream_ref(verbose=True))

@@ -33,9 +33,7 @@ __global__ void __launch_bounds__(NT) int8_rows_kernel(const Int8QuantArgs p) {
   uint32_t m = 0u;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    float v[8];
-    unpack8(rx[j], v);
-    m = amax8(v, m);
+    m = amax8_raw(rx[j], m);
   }
   const float a = __uint_as_float(row_max<L>(m, redm));
   if (l == 0 && live) p.row_amax[row] = a;

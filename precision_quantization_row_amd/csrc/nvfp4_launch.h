@@ -175,7 +175,8 @@ struct CacheArgs {
   int64_t B, cols;
   const int32_t *starts, *first;  // [B + 1], [B] or NULL
   const float* noop;
-  int64_t t0 = 0;
+  int64_t t0 = 0;      // the launch's first token
+  uint32_t h_inv = 0;  // ceil(2^32 / H)
 };
 int launch_cache_write(const CacheArgs& a, hipStream_t s);
 int launch_cache_read(const CacheArgs& a, hipStream_t s);

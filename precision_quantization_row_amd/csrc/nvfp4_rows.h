@@ -73,8 +73,13 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float* red) {
 template <int L>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   if constexpr (L <= 64) {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    // DPP: neighbour, pairs, half-row mirror, row mirror; the rest by shuffles
+    if constexpr (L >= 2) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));
+    if constexpr (L >= 4) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));
+    if constexpr (L >= 8) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));
+    if constexpr (L >= 16) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
+    if constexpr (L >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    if constexpr (L >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
     return v;
   } else {
     return block_max<L>(v, red);
@@ -89,11 +94,30 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
   return m;
 }
 
-// 8 values as E4M3 bytes: RN(v enc) clamped to 448 with the sign kept, to nearest even
+// The same of 8 elements as they lie in memory. (Two BF16 to an instruction.)
+__device__ __forceinline__ uint32_t amax8_raw(const Raw8<float>& r, uint32_t m) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, r.d[k] & kAbsF32);
+  return m;
+}
+__device__ __forceinline__ uint32_t amax8_raw(const Raw8<uint16_t>& r, uint32_t m) {
+  uint32_t p = r.d[0] & kAbsBf16x2;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) p = pk_max_u16(p, r.d[k] & kAbsBf16x2);
+  return max(m, max(p << 16, p & 0xFFFF0000u));
+}
+
+// 8 values as E4M3 bytes: RN(v enc) clamped to 448 with the sign kept, to nearest
+// even. CLAMP false: enc is RN(448 / a) of an a that no |v| passes, so that RN(v enc)
+// is at most 448 (1 + 2^-23), which rounds to 448, or not finite like a.
+template <bool CLAMP = true>
 __device__ __forceinline__ u32x2 pack8_e4m3(const float (&v)[8], float enc) {
   float t[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t[k] = fmaxf(fminf(v[k] * enc, kE4M3Max), -kE4M3Max);
+  for (int k = 0; k < 8; ++k) {
+    t[k] = v[k] * enc;
+    if (CLAMP) t[k] = fmaxf(fminf(t[k], kE4M3Max), -kE4M3Max);
+  }
   uint32_t w0 = 0u, w1 = 0u;
   w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], w0, false);
   w0 = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w0, true);
@@ -102,11 +126,13 @@ __device__ __forceinline__ u32x2 pack8_e4m3(const float (&v)[8], float enc) {
   return u32x2{w0, w1};
 }
 
-// The integer nearest to RN(v enc), halves to the even one, clamped to +-127, in
-// the low byte. 1.5 * 2^23 has steps of one and is even: adding it rounds so,
-// and the sum's low byte is the integer's two's complement.
+// The integer nearest to RN(v enc), halves to the even one, in the low byte. 1.5 *
+// 2^23 has steps of one and is even: adding it rounds so, and the sum's low byte is
+// the integer's two's complement. enc is RN(127 / a) of an a that no |v| passes:
+// RN(v enc) is at most 127 (1 + 2^-23), which rounds to 127, or not finite like a
+// (its byte says nothing then).
 __device__ __forceinline__ uint32_t int8_code(float v, float enc) {
-  return __float_as_uint(fmaxf(fminf(v * enc, kInt8Max), -kInt8Max) + 12582912.0f);
+  return __float_as_uint(v * enc + 12582912.0f);
 }
 // the low bytes of four dwords, a first
 __device__ __forceinline__ uint32_t pack4_low(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -137,8 +163,8 @@ __device__ __forceinline__ float line_top(int fmt, float F) {
   return fmt == FMT_E4M3 ? kE4M3Max : fmt == FMT_INT8 ? kInt8Max : F;
 }
 
-// Writes one lane's 8 values of a line as codes. NaN clamps to the top code in 8
-// bits: the line's amax, NaN as well, is what carries it. q, s: the line's
+// Writes one lane's 8 values of a line as codes. What 8-bit code a NaN gets says
+// nothing: the line's amax, NaN as well, is what carries it. q, s: the line's
 // first code and block scale; c: first element (a multiple of 8), n: elements
 // of the line from c on; a: the line's amax, enc: its encode scale. The lane
 // pair (2i, 2i + 1) holds one 16-element block; both lanes are active (lanes

@@ -75,8 +75,8 @@ class Cache:
             d = np.repeat((sc * a) * (f(1) / (f(bound) * f(6))), 16, -1)[..., :self.D]
             return unpack(q.reshape(-1, q.shape[-1]), self.D).astype(f).reshape(len(slot), self.H, self.D) * d
         if self.fmt == "e4m3":
-            return E4M3[q].astype(f) * (a / f(448))
-        return q.view(np.int8).astype(f) * (a / f(127))
+            return E4M3[q].astype(f) * (a * (f(1) / f(448)))
+        return q.view(np.int8).astype(f) * (a * (f(1) / f(127)))
 
     def check(self):
         assert np.array_equal(self.q.view(torch.uint8).cpu().numpy(), self.hq)
@@ -317,7 +317,7 @@ def test_offsets_past_32_bits():
     assert int((amax != 0).sum()) == 200 * H
     out = torch.empty(200, H, D, device=DEV)
     p.nvfp4_cache_read(out, None, q, None, amax, None, None, None, table, starts, first=first)
-    assert torch.equal(out, wq.view(200, H, D).float() * (wa / torch.full_like(wa, 127.0)).view(200, H, 1))
+    assert torch.equal(out, wq.view(200, H, D).float() * (wa * float(np.float32(1) / np.float32(127))).view(200, H, 1))
 
 
 def test_noop_stream_and_replay():
