@@ -7,11 +7,19 @@ namespace nvfp4 {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// 256 lines of A by 256 lines of B a workgroup of 4 waves, 128 x 128 a wave: its
-// sums take 256 of the lane's 512 registers. A stage is 128 bytes along k of all
-// 512 lines, 64 KB of LDS; two of them take turns.
+// 256 lines of A by 256 lines of B a workgroup of 4 waves, one wave a SIMD, 128 x
+// 128 a wave: its sums take 256 of the lane's 512 registers. A stage is 128 bytes
+// along k of all 512 lines, 64 KB of LDS; two of them take turns. A slice of a
+// stage is 32 k: 16 matrix instructions of 32 cycles from 8 fragments (64 bytes of
+// LDS a cycle for the CU), and beside them, one by one, the next slice's
+// fragments and the next stage but one's loads. The last slice of a stage holds
+// the barrier: by then everything of this stage is in registers and the next one
+// has landed, so the loads that follow may fill this stage's half.
+//
+// DIRECT: rows of whole 16-byte chunks at 16-byte addresses go straight from
+// memory into LDS. Others pass through registers, a stage ahead.
 constexpr int TM = 256, TN = 256, TK = 128;
-constexpr int SIDE = TM * TK, STAGE = 2 * SIDE;
+constexpr int SIDE = TM * TK;  // A's two halves, then B's
 // 16-byte slot s of line r, rotated by the line so that 16 lanes that read one
 // slot of 16 neighbouring lines touch all 64 banks once (a line is half of them).
 __device__ __forceinline__ int rotate(int r) {
@@ -29,7 +37,7 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, u
 template <bool DIRECT, bool GATED>
 __global__ void __launch_bounds__(256, 1) int8_tile_kernel(const GemmArgs p, int gm, int gn) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * SIDE];
   constexpr int OUT = GATED ? TN / 2 : TN;
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave & 1, wn = wave >> 1;
@@ -62,88 +70,134 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(const GemmArgs p, int
   const uint8_t* qu = GATED && (wave & 1) ? qb + p.N * K : qb;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
-  u32x4 ra[DIRECT ? 1 : 8], rb[DIRECT ? 1 : 8];
-  // the whole stage at k, which lies inside the lines, on its way to `buf`
-  auto fetch = [&](int k, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (DIRECT) {
-        const uint32_t at = lds0 + buf * STAGE + wave * 8192 + i * 1024;
-        load_to_lds(qa + k, aoff[i], at);
-        load_to_lds(qu + k, boff[i], at + SIDE);
-      } else {
-        ra[DIRECT ? 0 : i] = *reinterpret_cast<const u32x4_a1*>(qa + k + aoff[i]);
-        rb[DIRECT ? 0 : i] = *reinterpret_cast<const u32x4_a1*>(qu + k + boff[i]);
-      }
-    }
+  // chunk i of this thread: 0 .. 7 of A, 8 .. 15 of B, of the stage at k, which lies
+  // inside the lines
+  u32x4 ring[DIRECT ? 1 : 16];
+  auto fetch = [&](auto i_, int k, int half) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_)::value, j = i & 7;
+    // (the empty asm keeps the offset a 32-bit one added by the load itself)
+    uint32_t o = i < 8 ? aoff[j] : boff[j];
+    asm volatile("" : "+v"(o));
+    const uint8_t* base = (i < 8 ? qa : qu) + k;
+    if constexpr (DIRECT)
+      load_to_lds(base, o, lds0 + (i < 8 ? 0 : 2 * SIDE) + half * SIDE + wave * 8192 + j * 1024);
+    else
+      ring[DIRECT ? 0 : i] = *reinterpret_cast<const u32x4_a1*>(base + o);
   };
-  auto put = [&](int buf) __attribute__((always_inline)) {
-    if constexpr (!DIRECT) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = wave * 64 + 8 * i + lane / 8;
-        uint8_t* d = lds + buf * STAGE + r * TK + 16 * ((lane % 8) ^ rotate(r));
-        *reinterpret_cast<u32x4*>(d) = ra[DIRECT ? 0 : i];
-        *reinterpret_cast<u32x4*>(d + SIDE) = rb[DIRECT ? 0 : i];
-      }
-    }
+  auto put = [&](auto i_, int half) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_)::value;
+    const int r = wave * 64 + 8 * (i & 7) + lane / 8;
+    *reinterpret_cast<u32x4*>(lds + (i < 8 ? 0 : 2 * SIDE) + half * SIDE + r * TK + 16 * ((lane % 8) ^ rotate(r))) =
+        ring[DIRECT ? 0 : i];
   };
-  // a stage that reaches past the lines' end: zeros there
-  auto tail = [&](int k, int buf) {
+  // the same of a stage that reaches past the lines' end: zeros there
+  auto tail_chunk = [&](int i, int k) {
+    const int r = wave * 64 + 8 * (i & 7) + lane / 8, at = k + 16 * (lane % 8);
+    const uint8_t* line = i < 8 ? qa + (uint32_t)min(r, am) * K
+                                : qu + (uint32_t)min(GATED ? (r / 128) * 64 + r % 64 : r, bm) * K;
+    u32x4 w;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = keep_bytes(tail_dword(line, K, at + 4 * d), K - at - 4 * d);
+    return w;
+  };
+  // Any stage on its way: into its half (DIRECT) or the registers.
+  auto begin = [&](int u, int half) __attribute__((always_inline)) {
+    const int k = u * TK;
+    if (k + TK <= K) {
+      static_for<16>([&](auto i) __attribute__((always_inline)) { fetch(i, k, half); });
+    } else if constexpr (DIRECT) {
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      const int r = wave * 64 + 8 * (i & 7) + lane / 8, c = lane % 8;
-      const uint8_t* line = i < 8 ? qa + (uint32_t)min(r, am) * K
-                                  : qu + (uint32_t)min(GATED ? (r / 128) * 64 + r % 64 : r, bm) * K;
-      u32x4 w;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int at = k + 16 * c + 4 * d;
-        w[d] = keep_bytes(tail_dword(line, K, at), K - at);
+      for (int i = 0; i < 16; ++i) {
+        const int r = wave * 64 + 8 * (i & 7) + lane / 8;
+        *reinterpret_cast<u32x4*>(lds + (i < 8 ? 0 : 2 * SIDE) + half * SIDE + r * TK +
+                                  16 * ((lane % 8) ^ rotate(r))) = tail_chunk(i, k);
       }
-      *reinterpret_cast<u32x4*>(lds + buf * STAGE + (i < 8 ? 0 : SIDE) + r * TK + 16 * (c ^ rotate(r))) = w;
+    } else {
+      static_for<16>([&](auto i) __attribute__((always_inline)) { ring[DIRECT ? 0 : decltype(i)::value] = tail_chunk(decltype(i)::value, k); });
     }
   };
-
-  i32x16 acc[4][4] = {};
-  auto frag = [&](int buf, int side, int line, int s) __attribute__((always_inline)) {
-    return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + side * SIDE + line * TK + 16 * (s ^ rotate(l32)));
-  };
-  auto compute = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      i32x4 fa[4], fb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fa[i] = frag(buf, 0, wm * 128 + 32 * i + l32, 2 * d + g);
-        fb[i] = frag(buf, 1, wn * 128 + 32 * i + l32, 2 * d + g);
-      }
-#pragma unroll
-      for (int mi = 0; mi < 4; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < 4; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ni], fa[mi], acc[mi][ni], 0, 0, 0);
-    }
-  };
-  auto arrive = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0);  // (the loads into LDS are not the compiler's)
+  auto meet = [&]() __attribute__((always_inline)) {
+    if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): these loads are not the compiler's
     __syncthreads();
   };
-  const int nu = (K + TK - 1) / TK;
-  auto begin = [&](int u) __attribute__((always_inline)) {
-    if ((u + 1) * TK <= K) fetch(u * TK, u & 1);
-    else tail(u * TK, u & 1);
-  };
-  begin(0);
-  if (TK <= K) put(0);
-  arrive();
-#pragma unroll 1
-  for (int u = 0; u < nu; ++u) {
-    if (u + 1 < nu) begin(u + 1);
-    compute(u & 1);
-    if ((u + 2) * TK <= K) put((u + 1) & 1);
-    arrive();
+
+  // where this lane's fragments of slice d begin, of A's and B's first lines and halves
+  uint32_t pa[4], pb[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t o = l32 * TK + 16 * ((2 * d + g) ^ rotate(l32));
+    pa[d] = wm * 128 * TK + o;
+    pb[d] = 2 * SIDE + wn * 128 * TK + o;
   }
+  i32x16 acc[4][4] = {};
+  i32x4 fa[2][4], fb[2][4];
+  // fragment f of a slice, in the order that its products need them
+  auto read = [&](auto f_, auto d_, auto half_, i32x4 (&a)[4], i32x4 (&b)[4]) __attribute__((always_inline)) {
+    constexpr int F = decltype(f_)::value, D = decltype(d_)::value, H = decltype(half_)::value;
+    constexpr bool of_a = F == 0 || F > 4;
+    constexpr int i = F == 0 ? 0 : of_a ? F - 4 : F - 1;
+    const i32x4 v = *reinterpret_cast<const i32x4*>(lds + (of_a ? pa[D] : pb[D]) + H * SIDE + i * 32 * TK);
+    if constexpr (of_a) a[i] = v;
+    else b[i] = v;
+  };
+  // Slice D of stage u, which lies in half H. FAST: stage u + 2 lies inside the lines.
+  auto slice = [&](auto half_, auto d_, int u, auto fast_) __attribute__((always_inline)) {
+    constexpr int H = decltype(half_)::value, D = decltype(d_)::value, BAR = 3, CUR = D & 1, NXT = CUR ^ 1;
+    constexpr bool FAST = decltype(fast_)::value;
+    static_for<16>([&](auto n_) __attribute__((always_inline)) {
+      constexpr int n = decltype(n_)::value, mi = n / 4, ni = n % 4;
+      acc[mi][ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[CUR][ni], fa[CUR][mi], acc[mi][ni], 0, 0, 0);
+      if constexpr (D == 3 && n == BAR) meet();
+      constexpr int rd = D == 3 ? n - BAR - 1 : n;
+      if constexpr (rd >= 0 && rd < 8)
+        read(std::integral_constant<int, rd>{}, std::integral_constant<int, (D + 1) & 3>{},
+             std::integral_constant<int, D == 3 ? H ^ 1 : H>{}, fa[NXT], fb[NXT]);
+      if constexpr (DIRECT && FAST && D == 3 && n >= 8)
+        static_for<2>([&](auto x) __attribute__((always_inline)) {
+          fetch(std::integral_constant<int, 2 * (n - 8) + decltype(x)::value>{}, (u + 2) * TK, H);
+        });
+      if constexpr (!DIRECT && D < 3 && n % 3 == 2) {
+        constexpr int i = 5 * D + n / 3;  // 5 chunks a slice, the last one below
+        put(std::integral_constant<int, i>{}, H ^ 1);
+        if constexpr (FAST) fetch(std::integral_constant<int, i>{}, (u + 2) * TK, H);
+        if constexpr (i == 14) {
+          put(std::integral_constant<int, 15>{}, H ^ 1);
+          if constexpr (FAST) fetch(std::integral_constant<int, 15>{}, (u + 2) * TK, H);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  const int nu = (K + TK - 1) / TK;
+  auto stage = [&](auto half_, int u, auto fast_) __attribute__((always_inline)) {
+    slice(half_, std::integral_constant<int, 0>{}, u, fast_);
+    slice(half_, std::integral_constant<int, 1>{}, u, fast_);
+    slice(half_, std::integral_constant<int, 2>{}, u, fast_);
+    if constexpr (!DIRECT && !decltype(fast_)::value)
+      if (u + 2 < nu) begin(u + 2, decltype(half_)::value);
+    slice(half_, std::integral_constant<int, 3>{}, u, fast_);
+    if constexpr (DIRECT && !decltype(fast_)::value)
+      if (u + 2 < nu) begin(u + 2, decltype(half_)::value);
+  };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  begin(0, 0);
+  if constexpr (!DIRECT) static_for<16>([&](auto i) __attribute__((always_inline)) { put(i, 0); });
+  if (nu > 1) begin(1, 1);
+  meet();
+  static_for<8>([&](auto f) __attribute__((always_inline)) { read(f, C0{}, C0{}, fa[0], fb[0]); });
+  int u = 0;
+#pragma unroll 1
+  for (; (u + 4) * TK <= K; u += 2) {
+    stage(C0{}, u, std::true_type{});
+    stage(C1{}, u + 1, std::true_type{});
+  }
+#pragma unroll 1
+  for (; u < nu; u += 2) {
+    stage(C0{}, u, std::false_type{});
+    if (u + 1 < nu) stage(C1{}, u + 1, std::false_type{});
+  }
+  __syncthreads();  // the last fragments are read: LDS becomes the epilogue's
 
   // Epilogue, 32 lines of A at a time through LDS, so that a lane ends up with
   // 8 consecutive outputs of a line. Register r of a 32 x 32 result: line l32
