@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(const GemmArgs p, int
   // once a tile, and comes from L2 where it does not fit the instruction cache.)
   auto finish = [&](auto type_) __attribute__((always_inline)) {
     using T = decltype(type_);
-    constexpr int PARTS = GATED ? 2 : 4, PL = NL / PARTS;  // parts of 32 lines, accesses to one
+    constexpr int PARTS = 2, PL = NL / PARTS;  // parts of 32 lines, accesses to one
     Raw8<T> res[PL];
     load_residual<T, PL, RPL>(p, i00, j, nj, res);
 #pragma unroll 1
@@ -249,27 +249,39 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(const GemmArgs p, int
         __builtin_amdgcn_wave_barrier();
       }
       const int line = part * PL * RPL;  // of the wave's 128
-      float z0[PL][8], z1[PL][8];
+      // (every read of the part is on its way before the first is used)
+      i32x4 s0[PL][2], s1[GATED ? PL : 1][2];
+      LineScale xr[PL];
       Raw8<T> now[PL];
 #pragma unroll
       for (int v = 0; v < PL; ++v) {
         const int* row = ep + (line % 32 + lane / LPR + v * RPL) * PITCH;
         const float2 xs = *reinterpret_cast<const float2*>(row + 128);
-        const LineScale xr = {xs.x, __float_as_int(xs.y)};
-        if (all_plain) {
+        xr[v] = {xs.x, __float_as_int(xs.y)};
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            z0[v][q] = (float)row[cl + q] * (xr.m * w0[q].m) + b0[q];
-            if constexpr (GATED) z1[v][q] = (float)row[64 + cl + q] * (xr.m * w1[q].m) + b1[q];
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            z0[v][q] = apply_scale((float)row[cl + q], xr, w0[q]) + b0[q];
-            if constexpr (GATED) z1[v][q] = apply_scale((float)row[64 + cl + q], xr, w1[q]) + b1[q];
-          }
+        for (int h = 0; h < 2; ++h) {
+          s0[v][h] = *reinterpret_cast<const i32x4*>(row + cl + 4 * h);
+          if constexpr (GATED) s1[v][h] = *reinterpret_cast<const i32x4*>(row + 64 + cl + 4 * h);
         }
         now[v] = res[v];
+      }
+      float z0[PL][8], z1[PL][8];
+      if (all_plain) {
+#pragma unroll
+        for (int v = 0; v < PL; ++v)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            z0[v][q] = (float)s0[v][q / 4][q % 4] * (xr[v].m * w0[q].m) + b0[q];
+            if constexpr (GATED) z1[v][q] = (float)s1[v][q / 4][q % 4] * (xr[v].m * w1[q].m) + b1[q];
+          }
+      } else {
+#pragma unroll
+        for (int v = 0; v < PL; ++v)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            z0[v][q] = apply_scale((float)s0[v][q / 4][q % 4], xr[v], w0[q]) + b0[q];
+            if constexpr (GATED) z1[v][q] = apply_scale((float)s1[v][q / 4][q % 4], xr[v], w1[q]) + b1[q];
+          }
       }
       if (part + 1 < 4 * PARTS) load_residual<T, PL, RPL>(p, i00 + line + PL * RPL, j, nj, res);
       finish_lines<T, GATED, PL, RPL>(p, i00 + line, j, nj, z0, z1, now);
