@@ -1,79 +1,100 @@
 // int8_gemm_rows.hip -- the product of 8-bit integer lines for few lines of A
 // (gfx950).
-#include "gemm_device.h"
+#include "int8_device.h"
 
 namespace nvfp4 {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // For few lines of A (tokens) the product is bound by reading B. A workgroup
 // owns 16 NT lines of B and 16 MT lines of A; its 8 waves take the units of 128
 // k in turn, so that the workgroup reads runs of 1 KB of each line and no
-// workspace is needed: the waves' sums, exact integers, meet in LDS. Bytes go
-// straight from memory into the lanes that hold them as matrix fragments: lane
-// l has line l % 16 and bytes 32 (l / 16) .. + 31 of the unit, both operands
-// alike, so the sum covers every k once.
+// workspace is needed: the waves' sums, exact integers, meet in LDS. A matrix
+// fragment has 16 lines side by side in a wave's lanes; loaded so, each lane's 16
+// bytes are a request of their own (16 bytes a cycle and CU). Up to 16 lines of A that
+// does not hold up the stream of B; for more of them 8 lanes load 128 bytes of a
+// line, and the unit changes its order in the wave's own piece of LDS, where
+// nothing but the wave itself has to be waited for (128 x 4096 x 4096 14.0 -> 10.3 us,
+// 64 x 8192 x 8192 26.4 -> 23.6; 1 x 28672 x 8192 55.8 -> 59).
 constexpr int RW = 8;  // waves
 
 template <bool GATED, int MT, int NT>
 __global__ void __launch_bounds__(RW * 64) int8_few_kernel(const GemmArgs p, unsigned gn) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
   constexpr int PITCH = NT * 16 + 4, OT = GATED ? NT / 2 : NT, PD = MT == 1 ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) int part[RW][MT * 16 * PITCH];
+  constexpr bool TURN = MT > 1;                                           // through LDS
+  constexpr int UNIT = TURN ? (NT + MT) * 16 * 128 : 0, PART = MT * 16 * PITCH * 4;  // bytes a wave
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RW * (UNIT > PART ? UNIT : PART)];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   const int64_t i0 = (int64_t)(blockIdx.x / gn) * (16 * MT), j0 = (int64_t)(blockIdx.x % gn) * (16 * OT);
   const int K = (int)p.K;
   const int am = (int)min(p.M - i0, (int64_t)(16 * MT)) - 1, bm = (int)min(p.N - j0, (int64_t)(16 * OT)) - 1;
   const uint8_t *qa = p.a.q + i0 * K, *qb = p.b.q + j0 * K;
   const uint8_t* qu = GATED ? qb + p.N * K : qb;
-  // this lane's lines, from the tile's first (lines past the matrix repeat its
-  // last one; their products are not stored)
-  uint32_t ao[MT], bo[NT];
+  // Access t of a unit: this lane's chunk of line 8 t + lane / 8, or of line 16 (t / 2) +
+  // l16, the unit's first half or second. Offsets are from the tile's first line; lines
+  // past the matrix repeat its last one (their products are not stored).
+  auto line_at = [&](int t) { return TURN ? 8 * t + lane / 8 : 16 * (t / 2) + l16; };
+  auto byte_at = [&](int t) { return TURN ? 16 * (lane % 8) : 64 * (t & 1) + 16 * g; };
+  uint32_t ao[2 * MT], bo[2 * NT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) ao[t] = (uint32_t)min(16 * t + l16, am) * K + 32 * g;
+  for (int t = 0; t < 2 * MT; ++t) ao[t] = (uint32_t)min(line_at(t), am) * K + byte_at(t);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) bo[t] = (uint32_t)min(16 * (t % OT) + l16, bm) * K + 32 * g;
+  for (int t = 0; t < 2 * NT; ++t) bo[t] = (uint32_t)min(line_at(t % (2 * OT)), bm) * K + byte_at(t);
   struct Unit {
-    u32x4 a[MT][2], b[NT][2];
+    u32x4 a[2 * MT], b[2 * NT];
   } ring[PD];
   // Unit u; past the lines' end zeros.
   auto fetch = [&](Unit& r, int u) __attribute__((always_inline)) {
     const int k = 128 * u;
     if (k + 128 <= K) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < 2 * NT; ++t)
+        r.b[t] = *reinterpret_cast<const u32x4_a1*>((GATED && t >= 2 * OT ? qu : qb) + k + bo[t]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          r.b[t][h] = *reinterpret_cast<const u32x4_a1*>((GATED && t >= OT ? qu : qb) + k + 16 * h + bo[t]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) r.a[t][h] = *reinterpret_cast<const u32x4_a1*>(qa + k + 16 * h + ao[t]);
+      for (int t = 0; t < 2 * MT; ++t)
+        r.a[t] = *reinterpret_cast<const u32x4_a1*>(qa + k + ao[t]);
     } else {
-      const int kc = k + 32 * g;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const int at = kc + 4 * d;
+      for (int t = 0; t < 2 * NT; ++t)
+        r.b[t] = tail_chunk((GATED && t >= 2 * OT ? qu : qb) + bo[t] - byte_at(t), K, k + byte_at(t));
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          r.b[t][d / 4][d & 3] =
-              keep_bytes(tail_dword((GATED && t >= OT ? qu : qb) + bo[t] - 32 * g, K, at), K - at);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          r.a[t][d / 4][d & 3] = keep_bytes(tail_dword(qa + ao[t] - 32 * g, K, at), K - at);
-      }
+      for (int t = 0; t < 2 * MT; ++t) r.a[t] = tail_chunk(qa + ao[t] - byte_at(t), K, k + byte_at(t));
     }
   };
   i32x4 acc[MT][NT] = {};
+  uint8_t* own = lds + wave * UNIT;  // B's lines, then A's
+  uint8_t* to = own + (lane / 8) * 128;
+  const uint8_t* from = own + l16 * 128;
   auto multiply = [&](const Unit& r) __attribute__((always_inline)) {
+    if constexpr (TURN) {
+      // (a wave's LDS accesses are done in order: the last unit's reads precede)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int t = 0; t < 2 * (NT + MT); ++t)
+        *reinterpret_cast<u32x4*>(to + t * 1024 + 16 * ((lane % 8) ^ rotate(8 * t + lane / 8))) =
+            t < 2 * NT ? r.b[t < 2 * NT ? t : 0] : r.a[t < 2 * NT ? 0 : t - 2 * NT];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      i32x4 b[NT], a[MT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        b[n] = TURN ? *reinterpret_cast<const i32x4*>(from + n * 2048 + 16 * ((4 * h + g) ^ rotate(l16)))
+                    : __builtin_bit_cast(i32x4, r.b[2 * n + h]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        a[m] = TURN ? *reinterpret_cast<const i32x4*>(from + (NT + m) * 2048 + 16 * ((4 * h + g) ^ rotate(l16)))
+                    : __builtin_bit_cast(i32x4, r.a[2 * m + h]);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, r.b[n][h]),
-                                                            __builtin_bit_cast(i32x4, r.a[m][h]), acc[m][n], 0, 0, 0);
+          acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[n], a[m], acc[m][n], 0, 0, 0);
+    }
+    if constexpr (TURN) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
   };
   const int nu = (K + 127) / 128;
   static_for<PD>([&](auto i) __attribute__((always_inline)) {
@@ -89,6 +110,8 @@ __global__ void __launch_bounds__(RW * 64) int8_few_kernel(const GemmArgs p, uns
         if (u + RW * (I + PD) < nu) fetch(ring[I], u + RW * (I + PD));
       }
     });
+  __syncthreads();  // the units' LDS becomes the sums'
+  int(*part)[MT * 16 * PITCH] = reinterpret_cast<int(*)[MT * 16 * PITCH]>(lds);
   // register r of a 16 x 16 result: line l16 of A, line 4 g + r of B
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -169,7 +192,6 @@ static void launch_rows_t(const GemmArgs& a, hipStream_t s) {
     return go_rows<GATED, 1, GATED ? 2 : 1>(a, s);
   }
   if (mt <= 2) return go_rows<GATED, 2, 2>(a, s);
-  if (groups(4, 4) >= 256) return go_rows<GATED, 4, 4>(a, s);
   return go_rows<GATED, 4, 2>(a, s);
 }
 

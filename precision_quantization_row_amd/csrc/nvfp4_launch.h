@@ -227,7 +227,7 @@ void launch_gemm_rows(const GemmArgs& a, hipStream_t s);
 // scales, its factor 1 / 127
 bool int8_gemm_supported(int64_t M, int64_t N, int64_t K, bool gated);
 int launch_int8_gemm(const GemmArgs& a, hipStream_t s);
-void launch_int8_tile(const GemmArgs& a, hipStream_t s);
+void launch_int8_tile(const GemmArgs& a, int WM, hipStream_t s);
 void launch_int8_rows_gemm(const GemmArgs& a, hipStream_t s);
 
 }  // namespace nvfp4
