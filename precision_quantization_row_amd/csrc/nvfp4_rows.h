@@ -9,11 +9,36 @@ namespace nvfp4 {
 enum { FMT_NONE = 0, FMT_E4M3 = 1, FMT_NVFP4 = 2, FMT_INT8 = 3 };
 constexpr float kInt8Max = 127.0f;
 
+// Sum over each L lanes (a power of two up to 64), every lane gets it. Partners by DPP,
+// in a few cycles each where a shuffle goes through LDS: neighbour, pairs, half-row mirror,
+// row mirror, then the other 16 and 32 lanes. (After each step the lanes of a group hold
+// the same value, so a mirror joins the same groups as lane ^ 4 and lane ^ 8 would.)
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L >= 2) v = add_dpp<0xB1>(v);
+  if constexpr (L >= 4) v = add_dpp<0x4E>(v);
+  if constexpr (L >= 8) v = add_dpp<0x141>(v);
+  if constexpr (L >= 16) v = add_dpp<0x140>(v);
+  if constexpr (L >= 32) {
+    const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+  }
+  return v;
+}
+
 // Sum / max over a workgroup of NT threads; every thread gets the result.
 // `red` holds NT / 64 entries; consecutive calls use different ones.
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float* red) {
-  v = wave_sum(v);
+  v = lanes_sum<64>(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -41,9 +66,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
 template <int L>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   if constexpr (L <= 64) {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return lanes_sum<L>(v);
   } else {
     return block_sum<L>(v, red);
   }
@@ -51,11 +74,9 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 // two sums at once (red: 2 L / 64 entries)
 template <int L>
 __device__ __forceinline__ void row_sum2(float& u, float& v, float* red) {
-#pragma unroll
-  for (int o = (L < 64 ? L : 64) / 2; o > 0; o >>= 1) {
-    u += __shfl_xor(u, o);
-    v += __shfl_xor(v, o);
-  }
+  constexpr int P = L < 64 ? L : 64;
+  u = lanes_sum<P>(u);
+  v = lanes_sum<P>(v);
   if constexpr (L > 64) {
     if ((threadIdx.x & 63) == 0) {
       red[2 * (threadIdx.x >> 6)] = u;
