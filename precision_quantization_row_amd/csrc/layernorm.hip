@@ -258,42 +258,6 @@ int launch_layernorm(const LayerNormArgs& a, hipStream_t s) {
 // does not depend on timing. A workspace row holds dw, then db (those asked for).
 // 16384 x 4096 BF16 with dres: 94 us, 5.7 TB/s, and 4.9 us for the joining; 4097 x 2881
 // FP32 without: 29 us, 4.9 TB/s, and 5.2 us.
-// E elements as they lie in memory, at any element's address
-template <typename T, int E>
-struct Piece {
-  static constexpr int D = E * sizeof(T) / 4;
-  typedef uint32_t Words __attribute__((ext_vector_type(D)));
-  typedef Words Any __attribute__((aligned(sizeof(T))));
-  Words d;
-  template <bool NT = false>
-  __device__ __forceinline__ void load(const T* p) {
-    const Any* q = reinterpret_cast<const Any*>(p);
-    d = NT ? __builtin_nontemporal_load(q) : *q;
-  }
-  __device__ __forceinline__ void clear_first(int t) {
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if constexpr (sizeof(T) == 4) d[i] = i < t ? 0u : d[i];
-      else d[i] = 2 * i + 1 < t ? 0u : (2 * i < t ? d[i] & 0xFFFF0000u : d[i]);
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[E]) {
-    Words w;
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
-      else w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
-    }
-    __builtin_nontemporal_store(w, reinterpret_cast<Any*>(p));
-  }
-  __device__ __forceinline__ void get(float (&v)[E]) const {
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-      if constexpr (sizeof(T) == 4) v[k] = __uint_as_float(d[k]);
-      else v[k] = __uint_as_float(k & 1 ? d[k / 2] & 0xFFFF0000u : d[k / 2] << 16);
-    }
-  }
-};
 template <typename T, typename W, int L, int V, int NT>
 __global__ void __launch_bounds__(NT) ln_bwd_kernel(const LayerNormBwdArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;

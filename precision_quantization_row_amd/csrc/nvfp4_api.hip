@@ -426,8 +426,6 @@ int nvfp4_int8_quantize_rowcol(const void* x, int in_dtype, int64_t M, int64_t K
   if (!x || !row_amax || !col_amax || !q_row || !q_col || M < 1 || K < 1) return NVFP4_ERR_ARG;
   if (M > kMaxSize || K > kMaxSize || !valid_dtype(in_dtype)) return NVFP4_ERR_ARG;
   if (M > kMaxCols || K > kMaxCols) return NVFP4_ERR_UNSUPPORTED;
-  const int rc = nvfp4_amax_rowcol(x, in_dtype, M, K, row_amax, col_amax, nullptr, noop, 0, stream);
-  if (rc != NVFP4_OK) return rc;
   const Int8QuantArgs a = {x,        in_dtype, M, K, row_amax, col_amax, reinterpret_cast<uint8_t*>(q_row),
                            reinterpret_cast<uint8_t*>(q_col), noop};
   return launch_int8_rowcol(a, static_cast<hipStream_t>(stream)) ? NVFP4_ERR_HIP : NVFP4_OK;

@@ -157,7 +157,7 @@ struct Int8QuantArgs {
   int64_t row0 = 0;
 };
 int launch_int8_rows(const Int8QuantArgs& a, hipStream_t s);     // row_amax and q_row
-int launch_int8_rowcol(const Int8QuantArgs& a, hipStream_t s);   // both copies, from the amaxes
+int launch_int8_rowcol(const Int8QuantArgs& a, hipStream_t s);   // all four
 
 // pages of quantized lines (cache.hip); [0]: keys, [1]: values (q[1] NULL: none)
 struct CacheArgs {

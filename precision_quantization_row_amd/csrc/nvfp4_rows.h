@@ -107,6 +107,43 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   }
 }
 
+// E elements as they lie in memory, at any element's address
+template <typename T, int E>
+struct Piece {
+  static constexpr int D = E * sizeof(T) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(D)));
+  typedef Words Any __attribute__((aligned(sizeof(T))));
+  Words d;
+  template <bool NT = false>
+  __device__ __forceinline__ void load(const T* p) {
+    const Any* q = reinterpret_cast<const Any*>(p);
+    d = NT ? __builtin_nontemporal_load(q) : *q;
+  }
+  __device__ __forceinline__ void clear_first(int t) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      if constexpr (sizeof(T) == 4) d[i] = i < t ? 0u : d[i];
+      else d[i] = 2 * i + 1 < t ? 0u : (2 * i < t ? d[i] & 0xFFFF0000u : d[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[E]) {
+    Words w;
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+      else w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
+    }
+    __builtin_nontemporal_store(w, reinterpret_cast<Any*>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      if constexpr (sizeof(T) == 4) v[k] = __uint_as_float(d[k]);
+      else v[k] = __uint_as_float(k & 1 ? d[k / 2] & 0xFFFF0000u : d[k / 2] << 16);
+    }
+  }
+};
+
 // The second-level amax bits of 8 values joined to m. A NaN's bits lie above
 // every number's, so a line that holds one has a NaN amax.
 __device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
