@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gemm_device.h"
+#include "nvfp4_rows.h"
 
 namespace nvfp4 {
 

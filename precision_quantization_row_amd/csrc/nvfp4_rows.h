@@ -34,6 +34,18 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// Integers over a wave.
+__device__ __forceinline__ int lanes_sum_int(int v) {
+  v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false);
+  v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false);
+  v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, false);
+  v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, false);
+  const auto t = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = (int)(t[0] + t[1]);
+  const auto w = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  return (int)(w[0] + w[1]);
+}
+
 // Sum / max over a workgroup of NT threads; every thread gets the result.
 // `red` holds NT / 64 entries; consecutive calls use different ones.
 template <int NT>

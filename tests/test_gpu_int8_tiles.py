@@ -1,4 +1,4 @@
-"""The 8-bit integer product's tiles, each at sizes that its choice leads to, odd in every direction, against
+"""The 8-bit integer product's kernels, each at sizes that its choice leads to, odd in every direction, against
 64 bits: sums, bias, residual, z, the gated pair, operands and outputs at odd addresses.
 
 Tolerances: the sum's 8 roundings (U each), the bias' one, the residual's one, a rounding to the output's type.
@@ -18,6 +18,11 @@ PLAIN = {(64, 128): [(1030, 515, 101), (700, 700, 515)], (128, 128): [(4099, 260
          (256, 256): [(4099, 4101, 101), (4099, 4100, 304)]}
 GATED = {(64, 128): [(1030, 300, 101), (300, 700, 112)], (128, 128): [(4099, 1403, 515), (2059, 2601, 720)],
          (256, 256): [(4099, 2051, 101), (3001, 2601, 144)]}
+# one token to some dozens, lines of less than a run to many units, B that passes 128 MB
+FEW = [(1, 37, 5), (2, 130, 1025), (3, 1000, 4097), (4, 17, 1023), (1, 5, 16), (1, 1100, 122017), (2, 1100, 122017), (4, 1100, 122017),
+       (7, 1100, 122017), (16, 9000, 15001), (30, 1100, 122017), (50, 1100, 122017)]
+FEW_GATED = [(1, 9, 100), (2, 131, 1030), (3, 77, 2049), (4, 16, 15), (1, 560, 122017), (2, 560, 122017), (4, 560, 122017),
+             (7, 560, 122017), (30, 560, 122017), (50, 560, 122017)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -27,7 +32,7 @@ def _gpu():
     p.load_library()
 
 
-@pytest.mark.parametrize("M,N,K", [s for sizes in PLAIN.values() for s in sizes])
+@pytest.mark.parametrize("M,N,K", [s for sizes in PLAIN.values() for s in sizes] + FEW)
 def test_plain(M, N, K):
     say(f"[gpu] int8 tiles {M}x{N}x{K}")
     g = torch.Generator().manual_seed(M + N + K)
@@ -44,7 +49,7 @@ def test_plain(M, N, K):
         assert bool(((y.double() - want).abs() <= e + half * (want.abs() + e)).all())
 
 
-@pytest.mark.parametrize("M,N,K", [s for sizes in GATED.values() for s in sizes])
+@pytest.mark.parametrize("M,N,K", [s for sizes in GATED.values() for s in sizes] + FEW_GATED)
 def test_gated(M, N, K):
     say(f"[gpu] int8 tiles gated {M}x{N}x{K}")
     g = torch.Generator().manual_seed(M + N + K)
@@ -68,7 +73,7 @@ def test_gated(M, N, K):
         assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("M,N,K", [(1030, 515, 101), (4099, 2601, 515), (4099, 4100, 304)])
+@pytest.mark.parametrize("M,N,K", [(1, 333, 1111), (2, 333, 1111), (4, 333, 1111), (9, 333, 1111), (1030, 515, 101), (4099, 2601, 515), (4099, 4100, 304)])
 def test_any_address(M, N, K):
     g = torch.Generator().manual_seed(K)
     A, B = Lines(g, M, K), Lines(g, N, K)

@@ -46,8 +46,10 @@ def read(T, H, D, fmt, dt=0, v=True):
 
 
 # sizes of the GPU tests
-GEMM = [(1, 1, 1), (1, 4096, 4096), (16, 9000, 1111), (20, 300, 4097), (129, 300, 31), (512, 512, 2880), (1030, 515, 101), (4099, 2601, 515), (4099, 4101, 101)]
-GATED = [(1, 72, 200), (20, 33, 1000), (40, 66, 321), (1030, 300, 101), (4099, 1403, 515), (4099, 2051, 101)]
+GEMM = [(1, 1, 1), (16, 96, 1000), (2, 130, 1025), (3, 1000, 4097), (1, 1100, 122017), (2, 1100, 122017), (4, 1100, 122017), (7, 1100, 122017),
+        (16, 9000, 15001), (30, 1100, 122017), (50, 1100, 122017), (1, 4096, 4096), (16, 9000, 1111), (20, 300, 4097), (129, 300, 31), (512, 512, 2880), (1030, 515, 101), (4099, 2601, 515), (4099, 4101, 101)]
+GATED = [(1, 72, 200), (5, 96, 64), (2, 131, 1030), (3, 77, 2049), (1, 560, 122017), (2, 560, 122017), (4, 560, 122017), (7, 560, 122017),
+         (30, 560, 122017), (50, 560, 122017), (20, 33, 1000), (40, 66, 321), (1030, 300, 101), (4099, 1403, 515), (4099, 2051, 101)]
 ROWS = [(3, 7), (5, 512), (3, 513), (3, 2881), (2, 8192), (2, 16384), (1, 28672), (1, 50001)]
 BWD = [(50, 7), (2100, 96), (700, 512), (1100, 2048), (700, 4096), (600, 8192), (300, 16384), (300, 17000), (2, 40001)]
 HEADS = [(8, 64), (5, 40), (5, 100), (8, 128), (2, 129), (1, 192), (1, 257), (2, 512), (1, 1023), (2, 1024), (2, 7), (3, 250)]
