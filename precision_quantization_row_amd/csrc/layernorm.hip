@@ -314,18 +314,20 @@ __global__ void __launch_bounds__(NT) ln_bwd_kernel(const LayerNormBwdArgs p) {
   auto step = [&](int64_t r0, Row& a, float* rd) __attribute__((always_inline)) {
     const int64_t row = r0 + (G == 1 ? 0 : (int)threadIdx.x / L);
     const bool live = G == 1 || row < p.M;
-    const float r = a.r, mu = a.mu;
+    const float r = live ? a.r : 0.0f, mu = live ? a.mu : 0.0f;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       float dy[E], h[E], w[E];
       const int t = live ? twice[j] : E;
       if (!HOLD) rw[j].load(w_ + col[j]);
-      if (t > 0) {  // (all three: an infinity times zero)
+      // What is taken as zeros: dy and w (an infinity times zero is none), but not h: it is another
+      // lane's element of this row, so that xh is finite if the row's are ((0 - mu) r need not be).
+      if (t > 0) {
         a.dy[j].clear_first(t);
-        a.h[j].clear_first(t);
         if (!HOLD) rw[j].clear_first(t);
       }
+      if (!live) a.h[j].clear_first(E);  // (mu and r are zeros as well)
       a.dy[j].get(dy);
       a.h[j].get(h);
       rw[j].get(w);
@@ -457,9 +459,10 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LayerNormBwdArg
       load8(w + c, K - c, wv);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float g = dy[k] * wv[k];
+        // (past the row's end g is zero, and -mu r may be infinite)
+        const float g = dy[k] * wv[k], xh = k < K - c ? (h[k] - mu) * r : 0.0f;
         s1 += g;
-        s2 = __builtin_fmaf(g, (h[k] - mu) * r, s2);
+        s2 = __builtin_fmaf(g, xh, s2);
       }
     }
     row_sum2<NT>(s1, s2, red[turn]);
