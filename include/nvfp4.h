@@ -85,8 +85,9 @@ typedef enum {
                          the tensor), no block scales: value = byte * a / 448  */
   NVFP4_FMT_NVFP4 = 2, /* packed codes, block scales and amax, as above         */
   NVFP4_FMT_INT8 = 3  /* one signed byte an element in [-127, 127], one amax a
-                         line: value = byte * a / 127. The layer norm and the
-                         cache take it; nvfp4_gemm and nvfp4_rmsnorm do not     */
+                         line: value = byte * a / 127; bytes of zero where the
+                         amax is no finite number. The layer norm and the cache
+                         take it; nvfp4_gemm and nvfp4_rmsnorm do not           */
 } nvfp4_format;
 
 /* Activation of the product's epilogue. */
@@ -383,9 +384,9 @@ int64_t nvfp4_rmsnorm_backward_workspace(int64_t M, int64_t K);
  *          [-127, 127];  S = amax == 0 ? 1 : min(RN(127 / amax), FLT_MAX)
  * One pass: the amax is found and the codes are written by one read of the row.
  *   x [M][K] BF16 or FP32; row_amax [M] float, q [M][K]: both written
- * A row that holds a NaN gets a NaN amax, which makes every product of its codes
- * NaN; one that holds an infinity an infinite one (products infinite or NaN);
- * other rows are not affected. K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
+ * A row that holds a NaN gets a NaN amax, one that holds an infinity (and no NaN)
+ * an infinite one; the codes of both are zeros, and every product of them is NaN.
+ * Other rows are not affected. K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
 int nvfp4_int8_quantize(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax, int8_t* q,
                         const float* noop, void* stream);
 
@@ -393,7 +394,8 @@ int nvfp4_int8_quantize(const void* x, int in_dtype, int64_t M, int64_t K, float
  * rowwise for the forward product, columnwise (transposed) for the gradients'.
  * Enqueues nvfp4_amax_rowcol(x, ..., row_amax, col_amax, NULL, noop, 0, stream)
  * and one pass that writes both copies.
- *   row_amax [M], col_amax [K], q_row [M][K], q_col [K][M]: all written
+ *   row_amax [M], col_amax [K], q_row [M][K], q_col [K][M]: all written; NaN and
+ *   infinities as above, for rows and columns
  * M or K above 2^27 is NVFP4_ERR_UNSUPPORTED. */
 int nvfp4_int8_quantize_rowcol(const void* x, int in_dtype, int64_t M, int64_t K, float* row_amax,
                                float* col_amax, int8_t* q_row, int8_t* q_col, const float* noop,

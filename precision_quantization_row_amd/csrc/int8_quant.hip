@@ -4,6 +4,7 @@
 //   code = the integer nearest to RN(x * S), halves to the even one, clamped to
 //          +-127;  S = a == 0 ? 1 : min(RN(127 / a), FLT_MAX)
 //   value = code * a / 127
+// (a NaN or infinite: codes of zero)
 // Rows: one pass, the row held in registers between its amax and its codes. Both
 // copies: the amax pass first (a column's amax is not known before its last
 // row), then one pass that writes the rowwise and the transposed codes.
@@ -39,12 +40,13 @@ __global__ void __launch_bounds__(NT) int8_rows_kernel(const Int8QuantArgs p) {
   const float a = __uint_as_float(row_max<L>(m, redm));
   if (l == 0 && live) p.row_amax[row] = a;
   const float enc = global_encode_scale(a, kInt8Max);
+  const uint32_t keep = int8_keep(a);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int64_t c = 8 * (int64_t)(l + j * L);
     float v[8];
     unpack8(rx[j], v);
-    store8_bytes(p.q_row + row * p.K + c, K - c, pack8_int8(v, enc));
+    store8_bytes(p.q_row + row * p.K + c, K - c, pack8_int8(v, enc, keep));
   }
 }
 
@@ -65,10 +67,11 @@ __global__ void __launch_bounds__(1024) int8_rows_long_kernel(const Int8QuantArg
   const float a = __uint_as_float(block_max<NT>(m, redm));
   if (threadIdx.x == 0) p.row_amax[row] = a;
   const float enc = global_encode_scale(a, kInt8Max);
+  const uint32_t keep = int8_keep(a);
   for (int64_t c = 8 * (int64_t)threadIdx.x; c < K; c += 8 * NT) {
     float v[8];
     load8(x + c, K - c, v);
-    store8_bytes(p.q_row + row * K + c, K - c, pack8_int8(v, enc));
+    store8_bytes(p.q_row + row * K + c, K - c, pack8_int8(v, enc, keep));
   }
 }
 
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
   if (p.noop != nullptr && *p.noop == 1.0f) return;
   constexpr int PITCH = 33;  // dwords of a column's 128 rows, one to spare
   __shared__ uint32_t lds[128 * PITCH];
+  __shared__ uint32_t ckeep[128];
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
   const int64_t M = p.M, K = p.K;
   const int64_t i0 = row0 + 128 * (int64_t)(blockIdx.x / gn), j0 = 128 * (int64_t)(blockIdx.x % gn);
@@ -171,7 +175,11 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
   const bool whole = ((M | K) & 15) == 0;
   float ce[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) ce[k] = k < n ? global_encode_scale(p.col_amax[c + k], kInt8Max) : 0.0f;
+  for (int k = 0; k < 8; ++k) {
+    const float a = k < n ? p.col_amax[c + k] : 0.0f;
+    ce[k] = global_encode_scale(a, kInt8Max);
+    if (rg == 0) ckeep[8 * cg + k] = int8_keep(a);
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int64_t r = i0 + 64 * t + 4 * rg;
@@ -185,10 +193,11 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
       float x[8];
       unpack8(rx[v], x);
       if (r + v < M) {
-        const float enc = global_encode_scale(p.row_amax[r + v], kInt8Max);
+        const float a = p.row_amax[r + v], enc = global_encode_scale(a, kInt8Max);
+        const u32x2 codes = pack8_int8(x, enc, int8_keep(a));
         uint8_t* q = p.q_row + (r + v) * K + c;
-        if (whole && n >= 8) __builtin_nontemporal_store(pack8_int8(x, enc), reinterpret_cast<u32x2_a1*>(q));
-        else store8_bytes(q, n, pack8_int8(x, enc));
+        if (whole && n >= 8) __builtin_nontemporal_store(codes, reinterpret_cast<u32x2_a1*>(q));
+        else store8_bytes(q, n, codes);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) cc[v][k] = int8_code(x[k], ce[k]);
@@ -203,7 +212,8 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
     const int col = 32 * t + tid / 8, at = tid % 8;  // 16 rows of a column
     const int64_t j = j0 + col, i = i0 + 16 * at;
     if (j >= K || i >= M) continue;
-    const uint32_t* w = lds + col * PITCH + 4 * at;
+    const uint32_t *l = lds + col * PITCH + 4 * at, keep = ckeep[col];
+    const uint32_t w[4] = {l[0] & keep, l[1] & keep, l[2] & keep, l[3] & keep};
     uint8_t* q = p.q_col + j * M + i;
     if (i + 16 <= M) {
       if (whole) __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_a1*>(q));

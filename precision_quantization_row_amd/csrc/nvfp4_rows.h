@@ -199,22 +199,25 @@ __device__ __forceinline__ u32x2 pack8_e4m3(const float (&v)[8], float enc) {
 // The integer nearest to RN(v enc), halves to the even one, in the low byte. 1.5 *
 // 2^23 has steps of one and is even: adding it rounds so, and the sum's low byte is
 // the integer's two's complement. enc is RN(127 / a) of an a that no |v| passes:
-// RN(v enc) is at most 127 (1 + 2^-23), which rounds to 127, or not finite like a
-// (its byte says nothing then).
+// RN(v enc) is at most 127 (1 + 2^-23), which rounds to 127. Of an a that is no
+// number, the low byte is any: int8_keep clears it.
 __device__ __forceinline__ uint32_t int8_code(float v, float enc) {
   return __float_as_uint(v * enc + 12582912.0f);
 }
+// All ones for a line whose amax is a number, else zero: the codes of a line that holds a
+// NaN or an infinity are zeros, and its amax makes whatever is decoded from them NaN.
+__device__ __forceinline__ uint32_t int8_keep(float a) { return __float_as_uint(a) < 0x7F800000u ? ~0u : 0u; }
 // the low bytes of four dwords, a first
 __device__ __forceinline__ uint32_t pack4_low(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0C0C0400u);
   const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x0C0C0400u);
   return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
 }
-__device__ __forceinline__ u32x2 pack8_int8(const float (&v)[8], float enc) {
+__device__ __forceinline__ u32x2 pack8_int8(const float (&v)[8], float enc, uint32_t keep) {
   uint32_t t[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) t[k] = int8_code(v[k], enc);
-  return u32x2{pack4_low(t[0], t[1], t[2], t[3]), pack4_low(t[4], t[5], t[6], t[7])};
+  return u32x2{pack4_low(t[0], t[1], t[2], t[3]) & keep, pack4_low(t[4], t[5], t[6], t[7]) & keep};
 }
 
 // 8 bytes, or the first n of them
@@ -233,7 +236,7 @@ __device__ __forceinline__ float line_top(int fmt, float F) {
   return fmt == FMT_E4M3 ? kE4M3Max : fmt == FMT_INT8 ? kInt8Max : F;
 }
 
-// Writes one lane's 8 values of a line as codes. What 8-bit code a NaN gets says
+// Writes one lane's 8 values of a line as codes. What E4M3 byte a NaN gets says
 // nothing: the line's amax, NaN as well, is what carries it. q, s: the line's
 // first code and block scale; c: first element (a multiple of 8), n: elements
 // of the line from c on; a: the line's amax, enc: its encode scale. The lane
@@ -243,7 +246,7 @@ template <bool I8>
 __device__ __forceinline__ void write_codes(int fmt, uint8_t* q, uint8_t* s, int64_t c, int64_t n,
                                             const float (&y)[8], float a, float enc, float F_inv) {
   if (I8 && fmt == FMT_INT8) {
-    store8_bytes(q + c, n, pack8_int8(y, enc));
+    store8_bytes(q + c, n, pack8_int8(y, enc, int8_keep(a)));
   } else if (fmt == FMT_E4M3) {
     store8_bytes(q + c, n, pack8_e4m3(y, enc));
   } else {  // NVFP4
