@@ -82,7 +82,8 @@ enum { NVFP4_FLAG_FORCE_TWO_KERNEL = 1u }; /* skip the fused amax kernel */
 typedef enum {
   NVFP4_FMT_NONE = 0,
   NVFP4_FMT_E4M3 = 1, /* one E4M3 byte an element, one amax a line (or one for
-                         the tensor), no block scales: value = byte * a / 448  */
+                         the tensor), no block scales: value = byte * a / 448;
+                         no byte is a NaN: the amax of a line that holds one is */
   NVFP4_FMT_NVFP4 = 2, /* packed codes, block scales and amax, as above         */
   NVFP4_FMT_INT8 = 3  /* one signed byte an element in [-127, 127], one amax a
                          line: value = byte * a / 127; bytes of zero where the
@@ -476,7 +477,8 @@ int64_t nvfp4_layernorm_backward_workspace(int64_t M, int64_t K);
  *   amax [pages][page_size][H] float
  * Codes and scales are those of nvfp4_quantize_transpose's rowwise copy (NVFP4,
  * mode LINE), of nvfp4_rmsnorm (E4M3) and of nvfp4_int8_quantize (INT8), the
- * lines being rows.
+ * lines being rows; an E4M3 line that holds a NaN or an infinity gets bytes of
+ * zero, as an INT8 one does.
  * The tokens of a call lie one after another, sequence by sequence: sequence b has
  * tokens starts[b] .. starts[b + 1] - 1, at its positions first[b],
  * first[b] + 1, ... Position n lies at place n mod page_size of page

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheArgs p, int
       for (int j = 0; j < V; ++j) {
         const int c = 8 * (l + j * L);
         const int64_t n = !live ? 0 : EVEN ? (c < D ? 8 : 0) : D - c;
-        if constexpr (FMT == FMT_E4M3) store8_bytes(q + c, n, pack8_e4m3<false>(v[j], enc));
+        if constexpr (FMT == FMT_E4M3) store8_bytes(q + c, n, pack8_e4m3<false>(v[j], enc) & keep_finite(a));
         else write_codes<true>(FMT, q, s, c, n, v[j], a, enc, p.F_inv);
       }
     }

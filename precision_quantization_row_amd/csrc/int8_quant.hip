@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(NT) int8_rows_kernel(const Int8QuantArgs p) {
   const float a = __uint_as_float(row_max<L>(m, redm));
   if (l == 0 && live) p.row_amax[row] = a;
   const float enc = global_encode_scale(a, kInt8Max);
-  const uint32_t keep = int8_keep(a);
+  const uint32_t keep = keep_finite(a);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int64_t c = 8 * (int64_t)(l + j * L);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(1024) int8_rows_long_kernel(const Int8QuantArg
   const float a = __uint_as_float(block_max<NT>(m, redm));
   if (threadIdx.x == 0) p.row_amax[row] = a;
   const float enc = global_encode_scale(a, kInt8Max);
-  const uint32_t keep = int8_keep(a);
+  const uint32_t keep = keep_finite(a);
   for (int64_t c = 8 * (int64_t)threadIdx.x; c < K; c += 8 * NT) {
     float v[8];
     load8(x + c, K - c, v);
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
   for (int k = 0; k < 8; ++k) {
     const float a = k < n ? p.col_amax[c + k] : 0.0f;
     ce[k] = global_encode_scale(a, kInt8Max);
-    if (rg == 0) ckeep[8 * cg + k] = int8_keep(a);
+    if (rg == 0) ckeep[8 * cg + k] = keep_finite(a);
   }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) int8_cast_kernel(const Int8QuantArgs p, i
       unpack8(rx[v], x);
       if (r + v < M) {
         const float a = p.row_amax[r + v], enc = global_encode_scale(a, kInt8Max);
-        const u32x2 codes = pack8_int8(x, enc, int8_keep(a));
+        const u32x2 codes = pack8_int8(x, enc, keep_finite(a));
         uint8_t* q = p.q_row + (r + v) * K + c;
         if (whole && n >= 8) __builtin_nontemporal_store(codes, reinterpret_cast<u32x2_a1*>(q));
         else store8_bytes(q, n, codes);
