@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(const NormArgs p) {
     for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[j][k], h[j][k], ss);
     if (p.h) store8<true>(static_cast<T*>(p.h) + row * K + c, n, h[j]);
   }
-  ss = block_sum<NT>(ss, red);
+  ss = block_sum<NT, true>(ss, red);
   const float rstd = 1.0f / sqrtf(ss / (float)K + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   uint32_t m = 0u;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs p) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[k], h[k], ss);
   }
-  ss = block_sum<NT>(ss, red);
+  ss = block_sum<NT, true>(ss, red);
   const float rstd = 1.0f / sqrtf(ss / (float)K + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   uint32_t m = 0u;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormBwdArgs p) {
       }
     }
     // red[turn]: the other half is still being read by slower waves
-    const float mean = block_sum<NT>(dot, red[turn]) / (float)K;
+    const float mean = block_sum<NT, true>(dot, red[turn]) / (float)K;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int64_t c = 8 * ((int64_t)threadIdx.x + j * NT), n = K - c;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdArgs p
 #pragma unroll
       for (int k = 0; k < 8; ++k) dot = __builtin_fmaf(dy[k] * wv[k], h[k] * r, dot);
     }
-    const float mean = block_sum<NT>(dot, red[turn]) / (float)K;
+    const float mean = block_sum<NT, true>(dot, red[turn]) / (float)K;
     for (int64_t c = 8 * (int64_t)threadIdx.x; c < K; c += step) {
       const int64_t n = K - c;
       float dy[8], h[8], wv[8], dx[8];

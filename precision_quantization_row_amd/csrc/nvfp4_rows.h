@@ -34,6 +34,21 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// The same over a wave, partners 32, 16, 8, 4, 2 and 1 lanes apart in this order: sums of
+// floats depend on it. (After each step the lanes whose numbers differ by a multiple
+// of the step hold the same value, so that turning a row of 16 lanes by 8, 4, 2 or 1
+// joins the same sums as lane ^ 8 and so on.)
+__device__ __forceinline__ float wave_sum(float v) {
+  const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+  const auto u = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(u[0]) + __uint_as_float(u[1]);
+  v = add_dpp<0x128>(v);
+  v = add_dpp<0x124>(v);
+  v = add_dpp<0x122>(v);
+  return add_dpp<0x121>(v);
+}
+
 // Integers over a wave.
 __device__ __forceinline__ int lanes_sum_int(int v) {
   v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false);
@@ -47,10 +62,11 @@ __device__ __forceinline__ int lanes_sum_int(int v) {
 }
 
 // Sum / max over a workgroup of NT threads; every thread gets the result.
-// `red` holds NT / 64 entries; consecutive calls use different ones.
-template <int NT>
+// `red` holds NT / 64 entries; consecutive calls use different ones. FAR_FIRST: lanes
+// join as in wave_sum, else as in lanes_sum; the waves join in their order.
+template <int NT, bool FAR_FIRST = false>
 __device__ __forceinline__ float block_sum(float v, float* red) {
-  v = lanes_sum<64>(v);
+  v = FAR_FIRST ? wave_sum(v) : lanes_sum<64>(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();

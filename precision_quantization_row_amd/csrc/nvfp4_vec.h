@@ -182,12 +182,6 @@ __device__ __forceinline__ float dact_f(int act, float z) {
 }
 
 // ------------------------------------------------------------- reductions
-// Sum over the 64 lanes of a wave; every lane gets it. The order is fixed.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = row16_max(v);
   v = max(v, (uint32_t)__shfl_xor((int)v, 16));
