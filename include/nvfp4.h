@@ -393,8 +393,9 @@ int nvfp4_int8_quantize(const void* x, int in_dtype, int64_t M, int64_t K, float
 
 /* Both copies of X as lines of 8-bit integers, each direction with its own amax:
  * rowwise for the forward product, columnwise (transposed) for the gradients'.
- * Enqueues nvfp4_amax_rowcol(x, ..., row_amax, col_amax, NULL, noop, 0, stream)
- * and one pass that writes both copies.
+ * The amaxes are those of nvfp4_amax_rowcol, the rowwise copy that of
+ * nvfp4_int8_quantize. x is read twice: a column's amax is not known before its
+ * last row.
  *   row_amax [M], col_amax [K], q_row [M][K], q_col [K][M]: all written; NaN and
  *   infinities as above, for rows and columns
  * M or K above 2^27 is NVFP4_ERR_UNSUPPORTED. */

@@ -13,20 +13,25 @@ bool int8_gemm_supported(int64_t M, int64_t N, int64_t K, bool gated) {
 }
 
 // Which kernel runs: the few-lines one (0) or tiles of 64 WM lines of A (WM = 1, 2, 4; by
-// 128, 128 and 256 lines of B). Up to 32 lines B's bytes count alone: few-lines. For more, a
-// model of the four kernels' times in us, s stages of 128 k: a latency that a stage
-// costs however few the workgroups, and what n workgroups cost together (L2's and the
-// matrix pipe's share of a stage, the rest of a tile). Measured and modelled:
+// 128, 128 and 256 lines of B). Up to 32 lines always few-lines (32 x 4096 x 4096 7.6 us, the
+// quickest tile 16; 32 x 28672 x 8192 65 and 56). For more, a model of the four kernels'
+// times in us, s stages of 128 k: a latency that a stage costs however few the workgroups,
+// and what n workgroups cost together (L2's and the matrix pipe's share of a stage, the rest
+// of a tile). B's bytes from HBM are not in it: where they bound, its times are too
+// short, and only their order is of use. Measured and modelled:
 //                       few-lines      64 x 128       128 x 128      256 x 256
-//   128 x 4096 x 4096   9.8  12.9      14.9  15.2     18.9  17.7     48.2  50.2
-//   512 x 4096 x 4096   33.7 40.2      16.3  16.5     19.9  17.7     48.2  51.4
-//   1024 x 4096 x 4096  64.6 76.8      27.0  28.6     25.3  26.0     50.3  53.9
-//   4096 x 4096 x 4096  247              92.7  101    76.3  84.3     68.9  68.8
-//   512 x 8192 x 8192   140  136       46.8  48.9     41.0  42.3     84.1  91.8
-//   8192 x 1000 x 1000  92.4 62.5      26.1  21.9     21.2  20.8     32.8  29.4
-//   300 x 3000 x 300    10.5 8.0       7.0   6.6      9.4   8.1      22.7  19.7
-// Of 38 sizes from 1 x 64 x 64 to 4097 x 2880 x 2881 none took over 1.2 times the quickest
-// kernel's time, most within 1.05.
+//   128 x 4096 x 4096   10.3  12.7     15.0  15.2     18.4  17.7     47.6  50.2
+//   512 x 4096 x 4096   33.6  40.2     16.3  16.5     20.0  17.7     48.7  51.4
+//   1024 x 4096 x 4096  64.5  76.8     27.1  28.6     25.2  26.0     50.8  53.9
+//   4096 x 4096 x 4096  246   297      94.0  101      77.3  84.3     69.9  68.8
+//   512 x 8192 x 8192   138   136      47.6  49.0     41.1  42.3     86.2  91.8
+//   8192 x 1000 x 1000  94.3  61.7     26.3  21.9     20.7  20.8     32.8  26.7
+//   300 x 3000 x 300    11.1  8.1      7.2   5.8      9.4   7.8      23.0  19.3
+//   64 x 28672 x 8192   76.7  61.4     56.8  25.9     59.8  37.9     87.9  99.3
+//   256 x 28672 x 8192  258   235      108   82.5     80.9  69.2     98.5  99.3
+// Of 49 sizes from 8 x 300 x 5000 to 1024 x 28672 x 8192 none took over 1.2 times the
+// quickest kernel's time (1000 x 8192 x 301 1.18, 32 x 28672 x 8192 1.16, 8192 x 4096 x 256 1.12),
+// the others at most 1.05.
 static int tile_of(const GemmArgs& a) {
   if (a.M <= 32) return 0;
   const int64_t NB = a.act == 4 ? 2 * a.N : a.N;

@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(RW * 64) int8_few_kernel(const GemmArgs p, uns
 // no matrix fragment, so nothing has to change its order. A workgroup owns 4 R lines of
 // B (gated: half of them up lines); four of its waves take the units of 1024 k that are
 // even, four the others. A lane's sums are of its own 16 bytes in every KB; the lanes'
-// sums meet by DPP, the two waves' in LDS. 28672 x 8192: one line 38 us, 6.2 TB/s, two 41,
-// four 44 (the matrix kernel 54 for any; eight lines here 68); 8191 x 8191, one line: 13.6.
+// sums meet by DPP, the two waves' in LDS. 28672 x 8192: one line 42 us, 5.6 TB/s, two 38,
+// four 43 (the matrix kernel 54 for any; eight lines here 68); 8191 x 8191, one line: 13.6.
 template <bool GATED, int MV, int R, bool NT>
 __global__ void __launch_bounds__(512) int8_vec_kernel(const GemmArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
@@ -266,16 +266,16 @@ __global__ void __launch_bounds__(512) int8_vec_kernel(const GemmArgs p) {
 }
 
 // B of 128 MB, half the memory-side cache, and more is read past the caches: what a model
-// reads once a token is not there any more when the next token comes. (1 x 28672 x 8192
-// 40 -> 38 us, gated 80 -> 71; 8 lines, gated, 79 -> 70; but 1 x 4096 x 14336, 59 MB and read
-// again soon, 11 -> 13.)
+// reads once a token is not there any more when the next token comes. (Taken side
+// by side: 1 x 28672 x 8192 40 -> 38 us, gated 80 -> 71; 8 lines, gated, 79 -> 70; but
+// 1 x 4096 x 14336, 59 MB and read again soon, 11 -> 13.)
 static bool past_caches(const GemmArgs& a) { return (a.act == ACT_SWIGLU ? 2 : 1) * a.N * a.K >= (int64_t)128 << 20; }
 
 template <bool GATED, int MT, int NT>
 static void go_rows(const GemmArgs& a, hipStream_t s) {
   constexpr int OT = GATED ? NT / 2 : NT;
   const unsigned gn = (unsigned)((a.N + 16 * OT - 1) / (16 * OT));
-  const unsigned gm = (unsigned)((a.M + 16 * MT - 1) / (16 * MT));  // (few_lines bounds gm gn)
+  const unsigned gm = (unsigned)((a.M + 16 * MT - 1) / (16 * MT));  // (few lines, or few tiles: gm gn is at most 2^22)
   if (past_caches(a)) hipLaunchKernelGGL((int8_few_kernel<GATED, MT, NT, true>), dim3(gm * gn), dim3(RW * 64), 0, s, a, gn);
   else hipLaunchKernelGGL((int8_few_kernel<GATED, MT, NT, false>), dim3(gm * gn), dim3(RW * 64), 0, s, a, gn);
 }
@@ -290,8 +290,9 @@ static void go_vec(const GemmArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((int8_vec_kernel<GATED, MV, R, false>), g, b, 0, s, a);
 }
 
-// The tile of a few-lines launch: narrower ones where wide ones leave CUs without
-// a workgroup.
+// The tile of a few-lines launch. 5 to 16 lines, not gated, take 16 lines of B a workgroup
+// where 32 leave CUs without one; others always take the widest that their lines of A
+// allow, and up to four lines 16 of B.
 template <bool GATED>
 static void launch_rows_t(const GemmArgs& a, hipStream_t s) {
   const int64_t mt = (a.M + 15) / 16;

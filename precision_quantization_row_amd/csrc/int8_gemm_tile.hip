@@ -14,10 +14,14 @@ namespace nvfp4 {
 // and the loads of the stage after that. The last slice of a stage holds the
 // barrier: by then everything of this stage is in registers and the next one is in
 // LDS. (Loads straight into LDS, which aligned rows would allow, take longer: 8192^3
-// of zeros, where power does not count, 385 us against 360; of ordinary codes 8192 x 8192 x
-// 28672 with the residual takes 1514 us, 2.54 PFLOP/s, bound by the matrix pipe and power; half as long stages, four
+// of zeros, where power does not count, 385 us against 360; half as long stages, four
 // in turn, 381. Two groups of waves with every other stage each gain nothing: what
 // bounds few tiles is a CU's share of L2, 40 bytes a cycle.)
+// 8192 x 8192 x 28672 of ordinary codes with the residual: 1514 to 1596 us by the card, 2.41 to
+// 2.54 PO/s, the matrix pipe busy for 77 % of the cycles (counted), and power.
+// The compiler spills 16 registers of <false, 4, 4> and 14 of <true, 4, 4>, read in the loop of
+// the last stages (all stages of a product of fewer than four), and 11 of <false, 2, 2>, in
+// its epilogue; none in the loop of the others.
 constexpr int TK = 128;
 template <bool GATED, int WM, int WN>
 __global__ void __launch_bounds__(256, WM == 4 ? 1 : 2) int8_tile_kernel(const GemmArgs p, int gm, int gn) {

@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(1024) int8_rows_long_kernel(const Int8QuantArg
 // rows 43 us, 32 runs by 128 rows 13.6, 16 by 256 12.6; 16384 x 8192 BF16 with 64 runs by
 // 256 rows 68 us, 32 by 512 63, 16 by 512 72.
 // Of a tile's rows the first half is read past the caches, the second through them: the
-// cast reads all of x again right after, and finds what was read last. 16384 x 8192 BF16:
-// 63 us, 4.2 TB/s (53 where nothing before it is still being written out of the caches).
+// cast reads all of x again right after, and finds what was read last. 16384 x 8192 BF16,
+// one call after another: 63 to 70 us by the card, 3.9 TB/s (53 where nothing before it is
+// still being written out of the caches).
 constexpr int kAmaxRuns = 2, kAmaxRows = 512;
 template <typename T>
 __global__ void __launch_bounds__(256) int8_amax_kernel(const Int8QuantArgs p, int64_t row0, unsigned gn, int tr) {

@@ -159,7 +159,7 @@ struct Int8QuantArgs {
 int launch_int8_rows(const Int8QuantArgs& a, hipStream_t s);     // row_amax and q_row
 int launch_int8_rowcol(const Int8QuantArgs& a, hipStream_t s);   // all four
 
-// pages of quantized lines (cache.hip); [0]: keys, [1]: values (q[1] NULL: none)
+// pages of quantized lines (cache_write.hip, cache_read.hip); [0]: keys, [1]: values (q[1] NULL: none)
 struct CacheArgs {
   const void* src[2];  // write: [T][H][D], `stride` elements from token to token
   void* dst[2];        // read
