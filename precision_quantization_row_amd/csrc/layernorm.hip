@@ -15,8 +15,8 @@
 //   dw_k = sum over rows of dy_k * xh_k,   db_k = sum over rows of dy_k
 //
 // Both are bound by HBM: a row is read once into registers, reduced there and
-// written once. Forward, 16384 x 4096 BF16 with the residual: 95 us, 5.6 TB/s; one row of
-// 8192 4.6 us, a load's latency and the meetings of its waves.
+// written once. Forward, 16384 x 4096 BF16 with the residual: 95 to 98 us, 5.5 TB/s, into
+// 8-bit lines 81; one row of 8192 4.6 us, a load's latency and the meetings of its waves.
 #include "nvfp4_launch.h"
 #include "nvfp4_rows.h"
 
@@ -257,8 +257,9 @@ int launch_layernorm(const LayerNormArgs& a, hipStream_t s) {
 // groups join theirs in LDS, in order, and the sums go to row blockIdx.x of the
 // workspace, whose rows colsum_kernel adds in order: no atomics, so the result
 // does not depend on timing. A workspace row holds dw, then db (those asked for).
-// 16384 x 4096 BF16 with dres: 94 us, 5.7 TB/s, and 4.9 us for the joining; 4097 x 2881
-// FP32 without: 29 us, 4.9 TB/s, and 5.2 us.
+// 16384 x 4096 BF16 with dres: 94 to 97 us, 5.6 TB/s, and 5 us for the joining; 4097 x 2881
+// FP32 without: 29 to 31 us, 4.7 TB/s, and 5.2 us. Rows of 8193 to 16384 spill: 45 and 48
+// registers of FP32, 5 of BF16 with BF16 weights.
 template <typename T, typename W, int L, int V, int NT>
 __global__ void __launch_bounds__(NT) ln_bwd_kernel(const LayerNormBwdArgs p) {
   if (p.noop != nullptr && *p.noop == 1.0f) return;
